@@ -177,8 +177,8 @@ def _prepare_tensors(case, rand, dev):
         else:
             scales = [(st[k][a // BLOCK:a // BLOCK + n] for a, n in zip(starts, per)) if case["bits"] == 8 else
                       [None] * len(sizes) for k in ("m_scale", "v_scale")]
-            st["handle"] = AdamW(views(st["p"]), masters=views(st["master"]) if case["master"] else None,
-                                 bits=case["bits"], weight_decay=_decays(case), step=100, seed=SEED,
+            st["handle"] = AdamW(views(st["p"]), st["grads"], bits=case["bits"], weight_decay=_decays(case),
+                                 masters=views(st["master"]) if case["master"] else None, step=100, seed=SEED,
                                  states=list(zip(views(st["m"]), views(st["v"]), *scales)), **HYPER)
     return st
 
@@ -212,12 +212,12 @@ def run(state):
         if op == "norm_backward":
             return h.backward(state["x"], state["gamma"], state["beta"], state["mean"], state["rstd"], state["dy"])
         if op == "grad_norm":
-            control = h(state["grads"], max_norm=MAX_NORM, inv_scale=INV_SCALE)
+            control = h(max_norm=MAX_NORM, inv_scale=INV_SCALE)
             return dict(norm=control[0], coef=control[1])
         control = None
         if state["case"]["clip"]:
-            control = h.grad_norm(state["grads"], max_norm=MAX_NORM, inv_scale=INV_SCALE)
-        h.step(state["grads"], control=control)
+            control = h.grad_norm(max_norm=MAX_NORM, inv_scale=INV_SCALE)
+        h.step(control=control)
         return _updated(state, control)
     if op == "norm_forward":
         return _plain_norm_forward(state)
