@@ -175,8 +175,8 @@ def _prepare_tensors(case, rand, dev):
         if case["op"] == "grad_norm":
             st["handle"] = GradNorm(st["grads"])
         else:
-            scales = [(st[k][a // BLOCK:a // BLOCK + n] for a, n in zip(starts, per)) if case["bits"] == 8 else
-                      [None] * len(sizes) for k in ("m_scale", "v_scale")]
+            scales = [[st[k][a // BLOCK:a // BLOCK + n] if k in st else None for a, n in zip(starts, per)]
+                      for k in ("m_scale", "v_scale")]
             st["handle"] = AdamW(views(st["p"]), st["grads"], bits=case["bits"], weight_decay=_decays(case),
                                  masters=views(st["master"]) if case["master"] else None, step=100, seed=SEED,
                                  states=list(zip(views(st["m"]), views(st["v"]), *scales)), **HYPER)
