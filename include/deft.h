@@ -283,6 +283,82 @@ int deft_dwconv1d_forward(const float* x, const float* w, float* y, int batch, i
 int deft_dwpw1d_forward(const float* x, const float* w_dw, const float* w_pw, float* z, int batch, int steps,
                         int channels, int out_channels, int ksize, int dilation, void* stream);
 
+/* ---- The end of a training step: gradient norm and AdamW over a list of tensors ----
+ *
+ * Both take a host array that lists device tensors (dense, any number of
+ * elements, of one dtype); the list travels in the launches' arguments, so a
+ * call copies nothing to the device, keeps nothing, and can be captured in a
+ * HIP graph, which then replays on the same addresses.  count = 0 and tensors
+ * of no elements (whose pointers are not looked at) are allowed. */
+
+/* Elements that share one scale of an 8-bit state. */
+#define DEFT_STATE_BLOCK 256
+
+typedef struct deft_adamw_desc {
+  int p_dtype, g_dtype; /* enum deft_dtype of the weights and of the gradients */
+  int state_bits;       /* 32: m and v are fp32.  8: e4m3 codes with scales */
+  int master;           /* 1 (bf16 weights only): fp32 masters are updated, the weights are their
+                           rounded copies and are only written */
+  int64_t step;         /* this step's number, from 1 */
+  double lr, beta1, beta2, eps; /* lr, eps >= 0; 0 <= beta < 1 */
+  uint32_t seed;        /* 8-bit states: a new one for each step */
+} deft_adamw_desc;
+
+typedef struct deft_adamw_tensor {
+  void* p;              /* weights, updated */
+  const void* g;        /* gradient */
+  void* m;              /* first moment, updated: fp32, or e4m3 (OCP, 448 its largest value) codes */
+  void* v;              /* second moment, updated: fp32, or e4m3 codes of its square root */
+  float* m_scale;       /* 8-bit states: fp32 [ceil(n / DEFT_STATE_BLOCK)]; m = code * scale, */
+  float* v_scale;       /*   sqrt(v) = code * scale of its block of consecutive elements */
+  float* master;        /* fp32 master weights, updated (desc.master) */
+  int64_t n;            /* elements */
+  double weight_decay;  /* decoupled, >= 0 */
+} deft_adamw_tensor;
+
+/* One AdamW step over all listed tensors.  Per element, in fp32 with one
+ * rounding per operation, in this order:
+ *   g  = coef * grad                              (with control)
+ *   m  = beta1 * m + (1 - beta1) * g
+ *   v  = beta2 * v + (1 - beta2) * (g * g)
+ *   p  = p * (1 - lr * weight_decay)
+ *        - (m / (sqrt(v) / sqrt(1 - beta2^step) + eps)) * (lr / (1 - beta1^step))
+ * and p is rounded once to its dtype.  8-bit states: the step computes on code
+ * * scale; then scale = max|.| / 448 over each block, m is rounded to the
+ * nearest code, sqrt(v) to one of its two neighbours at random (unbiased, from
+ * a hash of seed, the tensor's number in the list and the element), and never
+ * from above zero to zero.  A block with a NaN or an infinity in m or v
+ * gets the scale NaN there.  Zeroed states (codes and scales) are a fresh
+ * start in both forms.
+ * control (device, may be NULL): what deft_grad_norm wrote.  Its factor
+ * multiplies the gradients; if it says that they are not finite, the step
+ * writes nothing.
+ * schedule (device, may be NULL): 4 doubles {lr, 1 - beta1^step, 1 -
+ * beta2^step, seed} that replace the descriptor's, read when the kernels run:
+ * for a captured step whose rates change from replay to replay.
+ * DEFT_ERR_DTYPE; DEFT_ERR_BAD_DESC (a negative size, a rate out of range,
+ * masters for fp32 weights); DEFT_ERR_UNSUPPORTED (over 2^31 - 1 workgroups of
+ * 1024 elements in one tensor); DEFT_ERR_NULLPTR; DEFT_ERR_ALIGN (tensors 16
+ * bytes, scales and control 4, schedule 8).  Checks run before any launch. */
+int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int count, const float* control,
+                    const double* schedule, void* stream);
+
+/* Norm of all listed gradients and the factor that clips them:
+ *   norm = sqrt(sum of squares) * inv_scale      (sums in fp64, fixed order)
+ *   factor = inv_scale * min(1, max_norm / (norm + 1e-6))
+ * with inv_scale > 0 the inverse of the loss's scale and max_norm > 0
+ * (infinity: no clipping).  Writes control (device, 4 floats): {norm, factor,
+ * 1 if every gradient is finite else 0, 0}; the factor is 0 where they are
+ * not.  No gradient is changed: deft_adamw_step applies the factor.
+ * DEFT_ERR_DTYPE, DEFT_ERR_BAD_DESC, DEFT_ERR_UNSUPPORTED, DEFT_ERR_NULLPTR,
+ * DEFT_ERR_ALIGN (gradients, control and workspace 16 bytes),
+ * DEFT_ERR_WORKSPACE; checks run before any launch. */
+int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtype, double max_norm,
+                   double inv_scale, float* control, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of deft_grad_norm for a list of `count` tensors. */
+size_t deft_grad_norm_workspace_bytes(int count);
+
 /* Per-kernel timing for benchmarks (host-side events only; no device memory).
  * deft_timing_start(capacity) creates `capacity` event pairs for the calling
  * thread; while active, each kernel that deft_forward / deft_backward /

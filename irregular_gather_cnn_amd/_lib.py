@@ -27,7 +27,8 @@ EXPORTED = ["deft_desc_validate", "deft_plan_create", "deft_plan_create_forced",
             "deft_backward",
             "deft_debug_sample_index", "deft_debug_sample", "deft_halo_histogram", "deft_error_string",
             "deft_last_hip_error", "deft_timing_start", "deft_timing_stop", "deft_timing_count",
-            "deft_timing_get", "deft_dwconv1d_forward", "deft_dwpw1d_forward"]
+            "deft_timing_get", "deft_dwconv1d_forward", "deft_dwpw1d_forward",
+            "deft_adamw_step", "deft_grad_norm", "deft_grad_norm_workspace_bytes"]
 
 
 class DeftError(RuntimeError):
@@ -56,6 +57,18 @@ class deft_plan_info(ctypes.Structure):
                 ("gather_gemm", ctypes.c_int), ("bwd_halo", ctypes.c_int)]
 
 
+class deft_adamw_desc(ctypes.Structure):
+    _fields_ = [("p_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int), ("state_bits", ctypes.c_int),
+                ("master", ctypes.c_int), ("step", ctypes.c_int64), ("lr", ctypes.c_double),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("seed", ctypes.c_uint32)]
+
+
+class deft_adamw_tensor(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("p", "g", "m", "v", "m_scale", "v_scale", "master")] + [
+        ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double)]
+
+
 _lib = None
 
 
@@ -68,7 +81,7 @@ def load() -> ctypes.CDLL:
         raise RuntimeError("libdeft.so is not built (%s); run irregular_gather_cnn_amd/build.py or "
                            "__graft_entry__.build()" % LIB_PATH)
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, i, sz, dbl = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
     dp = ctypes.POINTER(deft_desc)
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
@@ -88,6 +101,9 @@ def load() -> ctypes.CDLL:
         "deft_debug_sample_index": (i, [dp, vp, vp, vp, vp, vp]),
         "deft_debug_sample": (i, [vp, vp, vp, vp, vp]),
         "deft_halo_histogram": (i, [dp, vp, vp, i, vp]),
+        "deft_adamw_step": (i, [ctypes.POINTER(deft_adamw_desc), vp, i, vp, vp, vp]),
+        "deft_grad_norm": (i, [vp, vp, i, i, dbl, dbl, vp, vp, sz, vp]),
+        "deft_grad_norm_workspace_bytes": (sz, [i]),
         "deft_error_string": (ctypes.c_char_p, [i]),
         "deft_last_hip_error": (ctypes.c_char_p, []),
         "deft_timing_start": (i, [i]),
@@ -222,6 +238,22 @@ def deft_debug_sample(plan, x, offsets, cols, stream=None) -> None:
 def deft_halo_histogram(desc: deft_desc, offsets, hist, hist_len: int, stream=None) -> None:
     _check(load().deft_halo_histogram(ctypes.byref(desc), _ptr(offsets), _ptr(hist), int(hist_len),
                                       _ptr(stream)), "deft_halo_histogram")
+
+
+def deft_adamw_step(desc: deft_adamw_desc, tensors, count, control=None, schedule=None, stream=None) -> None:
+    """tensors: a ctypes array of deft_adamw_tensor (host)."""
+    _check(load().deft_adamw_step(ctypes.byref(desc), tensors, int(count), _ptr(control), _ptr(schedule),
+                                  _ptr(stream)), "deft_adamw_step")
+
+
+def deft_grad_norm(g, n, count, g_dtype, max_norm, inv_scale, control, workspace, ws_bytes, stream=None) -> None:
+    """g, n: ctypes arrays of c_void_p and c_int64 (host)."""
+    _check(load().deft_grad_norm(g, n, int(count), int(g_dtype), float(max_norm), float(inv_scale), _ptr(control),
+                                 _ptr(workspace), int(ws_bytes), _ptr(stream)), "deft_grad_norm")
+
+
+def deft_grad_norm_workspace_bytes(count: int) -> int:
+    return int(load().deft_grad_norm_workspace_bytes(int(count)))
 
 
 def deft_error_string(code: int) -> str:

@@ -125,4 +125,50 @@ struct BackwardArgs {
 };
 hipError_t launch_backward(const deft_plan& p, const BackwardArgs& a, hipStream_t s);
 
+// AdamW and the gradient norm over lists of tensors (deft_optim.hip).  A launch
+// carries its tensors in its arguments (under 4 KB), so a call copies nothing
+// to the device and can be captured; longer lists take several launches.
+constexpr int kStateBlock = DEFT_STATE_BLOCK;  // elements per scale of an 8-bit state
+constexpr int kAdamwElems = 4 * kStateBlock;   // per workgroup
+constexpr int kAdamwList = 40, kNormList = 64; // tensors per launch
+struct AdamwTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+  int64_t n;
+  double wd;
+  float decay;  // 1 - lr wd
+  uint32_t id;  // number in the call's list
+};
+struct AdamwArgs {
+  AdamwTensor t[kAdamwList];
+  uint32_t first[kAdamwList];  // first workgroup of each tensor
+  int count;
+  float b1, c1, b2, c2, eps, rate, low;
+  uint32_t seed;
+  const float* control;    // nullable
+  const double* schedule;  // nullable
+};
+static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
+hipError_t launch_adamw(const AdamwArgs& a, uint32_t blocks, int p_dtype, int g_dtype, int bits, bool master,
+                        hipStream_t st);
+constexpr int kNormPiece = 8192;      // elements a workgroup sums at a time
+constexpr uint32_t kNormGrid = 1024;  // workgroups, and partial sums, per launch
+struct GradNormArgs {
+  const void* g[kNormList];
+  int64_t n[kNormList];
+  uint32_t first[kNormList];  // first piece of each tensor
+  int count;
+  uint32_t pieces;
+  double* partials;
+};
+static_assert(sizeof(GradNormArgs) <= 4096, "kernel arguments");
+hipError_t launch_grad_squares(const GradNormArgs& a, int g_dtype, uint32_t grid, hipStream_t st);
+hipError_t launch_grad_norm(const double* partials, int count, double max_norm, double inv_scale, float* control,
+                            hipStream_t st);
+
 }  // namespace deft

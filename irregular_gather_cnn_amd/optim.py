@@ -1,0 +1,195 @@
+"""The end of a training step: gradient norm and AdamW over a list of tensors.
+
+PyTorch only supplies device memory and the stream; the arithmetic runs in
+libdeft.so (``deft_grad_norm``, ``deft_adamw_step``) through the binding in
+``_lib``.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+
+_DTYPES = {torch.float32: _lib.DEFT_F32, torch.bfloat16: _lib.DEFT_BF16}
+
+
+def _dtype_of(tensors, what):
+    kinds = {t.dtype for t in tensors}
+    if len(kinds) > 1 or not kinds <= set(_DTYPES):
+        raise TypeError("%s must all be float32 or all bfloat16, got %s" % (what, sorted(map(str, kinds))))
+    return _DTYPES[kinds.pop()] if kinds else _lib.DEFT_F32
+
+
+def _dense(t, what, device=None):
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (what, t.device, device))
+    return t
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+class _Gradients:
+    """The gradient buffers of a program: their sizes and dtype for good, the
+    buffers themselves until :meth:`bind` names others."""
+
+    def __init__(self, grads):
+        self.tensors = list(grads)
+        if not self.tensors:
+            raise ValueError("no gradients")
+        self.sizes = [g.numel() for g in self.tensors]
+        self.dtype = _dtype_of(self.tensors, "gradients")
+        self.device = self.tensors[0].device
+        self.pointers = (ctypes.c_void_p * len(self.sizes))()
+        self.bind(self.tensors)
+
+    def bind(self, grads):
+        grads = list(grads)
+        if len(grads) != len(self.sizes):
+            raise ValueError("%d gradients for %d tensors" % (len(grads), len(self.sizes)))
+        for k, (g, n) in enumerate(zip(grads, self.sizes)):
+            if g.numel() != n or _DTYPES.get(g.dtype) != self.dtype:
+                raise ValueError("gradient %d must have %d elements of the dtype of the first ones" % (k, n))
+            _dense(g, "gradient %d" % k, self.device)
+        self.tensors = grads
+        for k, g in enumerate(grads):
+            self.pointers[k] = g.data_ptr()
+
+
+class GradNorm:
+    """Norm of all gradients and the factor that clips them.
+
+    ``grads``: the gradient buffers (device tensors, all float32 or all
+    bfloat16), read at every call; :meth:`bind` names others of the same
+    sizes.  A call returns the device tensor ``control`` = {norm, factor, 1 if
+    all gradients are finite else 0, 0}, valid until the next call; nothing is
+    copied to the host."""
+
+    def __init__(self, grads):
+        self._setup(_Gradients(grads))
+
+    def _setup(self, grads):
+        self.grads = grads
+        count = len(grads.sizes)
+        self._n = (ctypes.c_int64 * count)(*grads.sizes)
+        self.ws_bytes = _lib.deft_grad_norm_workspace_bytes(count)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=grads.device)
+        self.control = torch.zeros(4, dtype=torch.float32, device=grads.device)
+
+    def bind(self, grads):
+        self.grads.bind(grads)
+
+    def __call__(self, max_norm=float("inf"), inv_scale=1.0):
+        g = self.grads
+        _lib.deft_grad_norm(g.pointers, self._n, len(g.sizes), g.dtype, max_norm, inv_scale, self.control, self.ws,
+                            self.ws_bytes, _stream(g.device))
+        return self.control
+
+
+class AdamW:
+    """AdamW with decoupled weight decay over ``params`` (device tensors, all
+    float32 or all bfloat16, updated in place) and their gradient buffers
+    ``grads`` (likewise; read at every step, :meth:`bind` names others).
+
+    ``bits``: 32 (fp32 states) or 8 (e4m3 codes of m and sqrt(v), one fp32
+    scale for each 256 elements).  ``masters``: None, True (fp32 copies of
+    bfloat16 params are made and updated, params are their rounded copies) or
+    a list of fp32 tensors.  ``weight_decay``: one number or one per tensor.
+    ``states``: None (zeros) or a list of (m, v, m_scale, v_scale) per param,
+    updated in place (the scales None with 32 bits), as :attr:`states` of an
+    earlier run whose :attr:`steps` is passed as ``step``."""
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32,
+                 masters=None, states=None, step=0, seed=0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no params")
+        if bits not in (8, 32):
+            raise ValueError("bits must be 8 or 32, got %r" % (bits,))
+        self.device = self.params[0].device
+        p_dtype = _dtype_of(self.params, "params")
+        for p in self.params:
+            _dense(p, "a param", self.device)
+        self.sizes = [p.numel() for p in self.params]
+        self.grads = _Gradients(grads)
+        if self.grads.sizes != self.sizes or self.grads.device != self.device:
+            raise ValueError("the gradients' sizes and device must be those of the params")
+        if masters is True:
+            masters = [p.float() for p in self.params]
+        self.masters = list(masters) if masters else None
+        if states is None:
+            states = [self._zero_state(n, bits) for n in self.sizes]
+        self.states = [tuple(s) for s in states]
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(self.params)
+        for what, got in (("masters", self.masters), ("states", self.states), ("weight decays", decay)):
+            if got is not None and len(got) != len(self.params):
+                raise ValueError("%d %s for %d params" % (len(got), what, len(self.params)))
+        self._check_states(bits)
+        self.lr, self.steps, self.seed = lr, int(step), int(seed)
+        self._desc = _lib.deft_adamw_desc(p_dtype, self.grads.dtype, bits, 1 if self.masters else 0, 0, lr, betas[0],
+                                          betas[1], eps, 0)
+        self._list = (_lib.deft_adamw_tensor * len(self.params))()
+        for k, p in enumerate(self.params):
+            m, v, ms, vs = self.states[k]
+            self._list[k] = _lib.deft_adamw_tensor(
+                p.data_ptr(), self.grads.pointers[k], m.data_ptr(), v.data_ptr(), ms.data_ptr() if bits == 8 else None,
+                vs.data_ptr() if bits == 8 else None, self.masters[k].data_ptr() if self.masters else None,
+                self.sizes[k], decay[k])
+        self._norm = GradNorm.__new__(GradNorm)
+        self._norm._setup(self.grads)
+
+    def bind(self, grads):
+        """From now on the gradients are read from these tensors."""
+        self.grads.bind(grads)
+        for item, g in zip(self._list, self.grads.pointers):
+            item.g = g
+
+    def _zero_state(self, n, bits):
+        if bits == 32:
+            return [torch.zeros(n, dtype=torch.float32, device=self.device) for _ in range(2)] + [None, None]
+        scales = -(-n // 256)
+        return [torch.zeros(n, dtype=torch.uint8, device=self.device).view(torch.float8_e4m3fn) for _ in range(2)] + [
+            torch.zeros(scales, dtype=torch.float32, device=self.device) for _ in range(2)]
+
+    def _check_states(self, bits):
+        kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        for k, n in enumerate(self.sizes):
+            want = [(t, n, kind, "state %d" % k) for t in self.states[k][:2]]
+            if bits == 8:
+                want += [(t, -(-n // 256), torch.float32, "scales of state %d" % k) for t in self.states[k][2:]]
+            if self.masters:
+                want.append((self.masters[k], n, torch.float32, "master %d" % k))
+            for t, size, dtype, what in want:
+                if t is None or t.numel() != size or t.dtype != dtype:
+                    raise ValueError("%s must have %d elements of %s" % (what, size, dtype))
+                _dense(t, what, self.device)
+
+    def grad_norm(self, max_norm=float("inf"), inv_scale=1.0):
+        """``control`` of the gradients (see :class:`GradNorm`), for :meth:`step`."""
+        return self._norm(max_norm, inv_scale)
+
+    def step_seed(self, step):
+        """The seed that rounds the 8-bit states of step number ``step``."""
+        return (self.seed + step * 0x9E3779B9) & 0xFFFFFFFF
+
+    def step(self, control=None, lr=None, schedule=None):
+        """One step.  ``control``: what :meth:`grad_norm` returned; its factor
+        multiplies the gradients and the step writes nothing if they are not
+        finite (it counts all the same).  ``lr``: from now on.  ``schedule``:
+        4 device doubles {lr, 1 - beta1^t, 1 - beta2^t, seed} that the kernels
+        read in place of the host's, for a step captured in a graph."""
+        if lr is not None:
+            self.lr = lr
+        for what, t, n, kind in (("control", control, 4, torch.float32), ("schedule", schedule, 4, torch.float64)):
+            if t is not None and (t.numel() != n or t.dtype != kind or t.device != self.device
+                                  or not t.is_contiguous()):
+                raise ValueError("%s must be %d contiguous elements of %s on %s" % (what, n, kind, self.device))
+        d = self._desc
+        d.lr, d.step, d.seed = self.lr, self.steps + 1, self.step_seed(self.steps + 1)
+        _lib.deft_adamw_step(d, self._list, len(self.params), control, schedule, _stream(self.device))
+        self.steps += 1
