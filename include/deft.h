@@ -283,6 +283,60 @@ int deft_dwconv1d_forward(const float* x, const float* w, float* y, int batch, i
 int deft_dwpw1d_forward(const float* x, const float* w_dw, const float* w_pw, float* z, int batch, int steps,
                         int channels, int out_channels, int ksize, int dilation, void* stream);
 
+/* ---- Group norm with an activation ----
+ *
+ * x is [n][c][s] (DEFT_CHANNELS_FIRST, as the convolution layer writes y) or
+ * [n][s][c] (DEFT_CHANNELS_LAST, as the 1-D convolutions do); a group is c /
+ * groups consecutive channels of one image.  Over each group's m = s * c /
+ * groups elements
+ *   mean = sum(x) / m,   rstd = 1 / sqrt(sum((x - mean)^2) / m + eps)
+ *   h = (x - mean) * rstd,   z = gamma * h + beta,   y = act(z)
+ * with act: none, relu max(z, 0), silu z / (1 + exp(-z)), gelu z * Phi(z) (Phi
+ * the normal distribution function, not its tanh approximation).  Statistics
+ * and all arithmetic are fp32; y is rounded once.  A NaN or an infinity in x
+ * makes its whole group's y NaN, and no other group's. */
+enum deft_layout { DEFT_CHANNELS_FIRST = 0, DEFT_CHANNELS_LAST = 1 };
+enum deft_act { DEFT_ACT_NONE = 0, DEFT_ACT_RELU = 1, DEFT_ACT_SILU = 2, DEFT_ACT_GELU = 3 };
+
+typedef struct deft_norm_desc {
+  int n, c, s;   /* images, channels, positions (h * w, or steps) */
+  int groups;    /* divides c */
+  int layout;    /* enum deft_layout */
+  int act;       /* enum deft_act */
+  int dtype;     /* enum deft_dtype of x, gamma, beta, y and the gradients */
+  double eps;    /* >= 0 */
+} deft_norm_desc;
+
+/* DEFT_OK, or the code with which the calls below refuse the descriptor. */
+int deft_norm_desc_validate(const deft_norm_desc* d);
+
+/* Workspace bytes of deft_norm_forward (training = 0) or deft_norm_backward
+ * (training = 1); 0 for a descriptor that they refuse. */
+size_t deft_norm_workspace_bytes(const deft_norm_desc* d, int training);
+
+/* y = act(group norm of x), and mean and rstd (fp32 [n][groups], written) as
+ * deft_norm_backward takes them.  y must not overlap x.  n = 0 or s = 0 is a
+ * no-op that checks no pointer.
+ * DEFT_ERR_BAD_DESC (a negative size, c, eps or enum out of range; y over x),
+ * DEFT_ERR_GROUPS (groups < 1 or not a divisor of c), DEFT_ERR_DTYPE,
+ * DEFT_ERR_UNSUPPORTED (more than 2048 channels per group, or 2^31 - 1
+ * workgroups), DEFT_ERR_NULLPTR, DEFT_ERR_ALIGN (every pointer 16 bytes),
+ * DEFT_ERR_WORKSPACE; checks run before any launch. */
+int deft_norm_forward(const deft_norm_desc* d, const void* x, const void* gamma, const void* beta, void* y,
+                      float* mean, float* rstd, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients at dy, with mean and rstd as the forward left them:
+ *   dz = dy * act'(z)     (relu: dy where z > 0, else 0)
+ *   dbeta = sum dz,  dgamma = sum dz * h          (over images and positions)
+ *   dx = rstd * (gamma dz - mean_group(gamma dz) - h * mean_group(gamma dz h))
+ * dx, dgamma and dbeta are written, each rounded once; any of them may be NULL
+ * and is not computed then.  All sums run in a fixed order: a call repeats its
+ * bits.  dx must overlap neither x nor dy.  n = 0 or s = 0 writes zeros to
+ * dgamma and dbeta.  Errors as for deft_norm_forward. */
+int deft_norm_backward(const deft_norm_desc* d, const void* x, const void* gamma, const void* beta,
+                       const float* mean, const float* rstd, const void* dy, void* dx, void* dgamma, void* dbeta,
+                       void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- The end of a training step: gradient norm and AdamW over a list of tensors ----
  *
  * Both take a host array that lists device tensors (dense, any number of

@@ -28,7 +28,11 @@ EXPORTED = ["deft_desc_validate", "deft_plan_create", "deft_plan_create_forced",
             "deft_debug_sample_index", "deft_debug_sample", "deft_halo_histogram", "deft_error_string",
             "deft_last_hip_error", "deft_timing_start", "deft_timing_stop", "deft_timing_count",
             "deft_timing_get", "deft_dwconv1d_forward", "deft_dwpw1d_forward",
-            "deft_adamw_step", "deft_grad_norm", "deft_grad_norm_workspace_bytes"]
+            "deft_adamw_step", "deft_grad_norm", "deft_grad_norm_workspace_bytes",
+            "deft_norm_desc_validate", "deft_norm_workspace_bytes", "deft_norm_forward",
+            "deft_norm_backward"]
+LAYOUTS = {"channels_first": 0, "channels_last": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
 class DeftError(RuntimeError):
@@ -69,6 +73,11 @@ class deft_adamw_tensor(ctypes.Structure):
         ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double)]
 
 
+class deft_norm_desc(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int) for k in ("n", "c", "s", "groups", "layout", "act", "dtype")] + [
+        ("eps", ctypes.c_double)]
+
+
 _lib = None
 
 
@@ -104,6 +113,10 @@ def load() -> ctypes.CDLL:
         "deft_adamw_step": (i, [ctypes.POINTER(deft_adamw_desc), vp, i, vp, vp, vp]),
         "deft_grad_norm": (i, [vp, vp, i, i, dbl, dbl, vp, vp, sz, vp]),
         "deft_grad_norm_workspace_bytes": (sz, [i]),
+        "deft_norm_desc_validate": (i, [ctypes.POINTER(deft_norm_desc)]),
+        "deft_norm_workspace_bytes": (sz, [ctypes.POINTER(deft_norm_desc), i]),
+        "deft_norm_forward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 7 + [sz, vp]),
+        "deft_norm_backward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 10 + [sz, vp]),
         "deft_error_string": (ctypes.c_char_p, [i]),
         "deft_last_hip_error": (ctypes.c_char_p, []),
         "deft_timing_start": (i, [i]),
@@ -254,6 +267,26 @@ def deft_grad_norm(g, n, count, g_dtype, max_norm, inv_scale, control, workspace
 
 def deft_grad_norm_workspace_bytes(count: int) -> int:
     return int(load().deft_grad_norm_workspace_bytes(int(count)))
+
+
+def deft_norm_desc_validate(desc: deft_norm_desc) -> None:
+    _check(load().deft_norm_desc_validate(ctypes.byref(desc)), "deft_norm_desc_validate")
+
+
+def deft_norm_workspace_bytes(desc: deft_norm_desc, training: int) -> int:
+    return int(load().deft_norm_workspace_bytes(ctypes.byref(desc), int(training)))
+
+
+def deft_norm_forward(desc: deft_norm_desc, x, gamma, beta, y, mean, rstd, workspace, ws_bytes, stream=None) -> None:
+    _check(load().deft_norm_forward(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
+                                    _ptr(rstd), _ptr(workspace), int(ws_bytes), _ptr(stream)), "deft_norm_forward")
+
+
+def deft_norm_backward(desc: deft_norm_desc, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta, workspace, ws_bytes,
+                       stream=None) -> None:
+    _check(load().deft_norm_backward(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
+                                     _ptr(dy), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), int(ws_bytes),
+                                     _ptr(stream)), "deft_norm_backward")
 
 
 def deft_error_string(code: int) -> str:

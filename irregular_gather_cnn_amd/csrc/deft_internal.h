@@ -171,4 +171,40 @@ hipError_t launch_grad_squares(const GradNormArgs& a, int g_dtype, uint32_t grid
 hipError_t launch_grad_norm(const double* partials, int count, double max_norm, double inv_scale, float* control,
                             hipStream_t st);
 
+// Group norm with activation (deft_norm_fwd.hip, deft_norm_bwd.hip).  A group
+// of an image, or a band of whole groups where channels come last, is cut into
+// `slices` that one workgroup each holds in registers.  One slice: statistics
+// and result in one launch.  More: partial statistics, their combination, and
+// the result from a second read.
+constexpr int kNormThreads = 512;
+enum NormMode { kNormWhole = 0, kNormStats = 1, kNormApply = 2 };
+struct NormArgs {
+  const void* x;
+  const void* dy;     // backward
+  const void* gamma;
+  const void* beta;
+  void* out;          // y, or dx (nullable)
+  float* mean;        // [n][g]: written forward, read backward
+  float* rstd;
+  float* part;        // partial sums, one block per slice: see each kernel
+  float* sums;        // backward, several slices: [n][g][2] sums of gamma dz and of gamma dz h
+  int n, c, s, g, per, act;
+  float eps;
+  int slices, rp;     // channels last: rows (positions) per slice; first: channels per slice
+  int bands;          // channels last
+  int ws, cp;         // channels first: slices along the positions, and positions in each
+  int lt;             // channels first: log2 of the lanes that share a channel's positions
+};
+struct NormPlan {     // how a call is cut
+  int vec, u, threads;  // elements per access, accesses per thread, threads per workgroup
+  uint32_t blocks;
+  size_t lds;
+};
+hipError_t launch_norm_fwd(const NormArgs& a, const NormPlan& p, int layout, int dtype, int mode, hipStream_t st);
+hipError_t launch_norm_bwd(const NormArgs& a, const NormPlan& p, int layout, int dtype, int mode, hipStream_t st);
+hipError_t launch_norm_combine(const NormArgs& a, int layout, hipStream_t st);
+hipError_t launch_norm_bwd_sums(const NormArgs& a, int layout, int dtype, hipStream_t st);
+hipError_t launch_norm_params(const float* part, int rows, int c, void* dgamma, void* dbeta, int dtype,
+                              hipStream_t st);
+
 }  // namespace deft

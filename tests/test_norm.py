@@ -1,0 +1,411 @@
+"""Group norm with activation (deft_norm_forward, deft_norm_backward).
+
+CPU: the oracle against torch and against differences, and every refusal of
+the C ABI and of the Python class.  GPU: against the oracle in float64, within
+bounds that count the kernels' roundings (oracle/norm.py).
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from irregular_gather_cnn_amd import _lib as L
+from irregular_gather_cnn_amd.norm import GroupNormAct
+from oracle import norm as O
+
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+ACTS = ["none", "relu", "silu", "gelu"]
+LAYOUTS = ["channels_first", "channels_last"]
+
+
+# ------------------------------------------------------------------ CPU: oracle
+
+@pytest.mark.parametrize("name", ACTS)
+def test_oracle_is_torchs(name):
+    r = np.random.default_rng(0)
+    n, c, s, g = 2, 12, 7, 3
+    x, dy = r.standard_normal((2, n, c, s))
+    gamma, beta = r.standard_normal((2, c))
+    xt, gt, bt = (torch.from_numpy(v.copy()).requires_grad_() for v in (x, gamma, beta))
+    fn = dict(none=lambda z: z, relu=torch.relu, silu=torch.nn.functional.silu, gelu=torch.nn.functional.gelu)[name]
+    y = fn(torch.nn.functional.group_norm(xt, g, gt, bt, 1e-3))
+    y.backward(torch.from_numpy(dy))
+    f = O.forward(x, gamma, beta, g, 1e-3, name, "f32")
+    np.testing.assert_allclose(f["y"][0], y.detach().numpy(), rtol=1e-12, atol=1e-13)
+    b = O.backward(x, gamma, beta, f["mean"][0], f["rstd"][0], dy, g, name, "f32")
+    for k, t in (("dx", xt), ("dgamma", gt), ("dbeta", bt)):
+        np.testing.assert_allclose(b[k][0], t.grad.numpy(), rtol=1e-10, atol=1e-12)
+
+
+@pytest.mark.parametrize("name", ["none", "silu", "gelu"])
+def test_oracle_gradient_against_differences(name):
+    r = np.random.default_rng(1)
+    x, dy = r.standard_normal((2, 2, 6, 5))
+    gamma, beta = r.standard_normal((2, 6))
+
+    def loss(x, gamma, beta):
+        return (O.forward(x, gamma, beta, 2, 1e-3, name, "f32")["y"][0] * dy).sum()
+
+    f = O.forward(x, gamma, beta, 2, 1e-3, name, "f32")
+    grads = O.backward(x, gamma, beta, f["mean"][0], f["rstd"][0], dy, 2, name, "f32")
+    for key, v in (("dx", x), ("dgamma", gamma), ("dbeta", beta)):
+        flat = v.reshape(-1)
+        for i in range(0, flat.size, 3):
+            keep, e = flat[i], 1e-5
+            flat[i] = keep + e
+            up = loss(x, gamma, beta)
+            flat[i] = keep - e
+            down = loss(x, gamma, beta)
+            flat[i] = keep
+            assert abs((up - down) / (2 * e) - grads[key][0].reshape(-1)[i]) < 1e-7
+
+
+# ------------------------------------------------------------------ CPU: refusals
+
+FAKE = 0x10000
+
+
+def desc(n=2, c=32, s=10, groups=4, layout=1, act=1, dtype=1, eps=1e-5):
+    return L.deft_norm_desc(n, c, s, groups, layout, act, dtype, eps)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), -1), (dict(s=-1), -1), (dict(c=0), -1), (dict(layout=2), -1), (dict(layout=-1), -1),
+    (dict(act=4), -1), (dict(act=-1), -1), (dict(dtype=2), -6), (dict(dtype=-1), -6), (dict(eps=-1e-9), -1),
+    (dict(eps=math.nan), -1), (dict(eps=math.inf), -1), (dict(groups=0), -2), (dict(groups=5), -2),
+    (dict(c=2049, groups=1), -10), (dict(n=1 << 30, groups=32), -10), (dict(), 0), (dict(n=0), 0),
+    (dict(c=2048, groups=1), 0), (dict(eps=0.0), 0)])
+def test_descriptor_refusals(kw, code):
+    lib, d = L.load(), desc(**kw)
+    assert lib.deft_norm_desc_validate(ctypes.byref(d)) == code
+    if code:
+        assert lib.deft_norm_workspace_bytes(ctypes.byref(d), 1) == 0
+        args = [None] * 7 + [0, None]
+        assert lib.deft_norm_forward(ctypes.byref(d), *args) == code
+        assert lib.deft_norm_backward(ctypes.byref(d), *[None] * 10, 0, None) == code
+
+
+def test_null_descriptor_and_empty_calls():
+    lib = L.load()
+    assert lib.deft_norm_desc_validate(None) == -4
+    assert lib.deft_norm_workspace_bytes(None, 0) == 0
+    assert lib.deft_norm_forward(None, *[None] * 7, 0, None) == -4
+    for kw in (dict(n=0), dict(s=0)):
+        d = desc(**kw)
+        assert lib.deft_norm_forward(ctypes.byref(d), *[None] * 7, 0, None) == 0
+        assert lib.deft_norm_backward(ctypes.byref(d), *[None] * 10, 0, None) == 0
+
+
+@pytest.mark.fake_pointers
+@pytest.mark.parametrize("layout", [0, 1])
+def test_pointer_refusals(layout):
+    lib, d = L.load(), desc(n=2, c=32, s=100000, layout=layout)
+    ws = lib.deft_norm_workspace_bytes(ctypes.byref(d), 0)
+    assert ws > 0  # a shape that is cut into slices
+    far = 1 << 30
+    fwd = dict(x=FAKE, gamma=FAKE, beta=FAKE, y=far, mean=FAKE, rstd=FAKE, ws=FAKE, bytes=ws, stream=None)
+    bwd_ws = lib.deft_norm_workspace_bytes(ctypes.byref(d), 1)
+    bwd = dict(x=FAKE, gamma=FAKE, beta=FAKE, mean=FAKE, rstd=FAKE, dy=FAKE, dx=far, dgamma=FAKE, dbeta=FAKE,
+               ws=FAKE, bytes=bwd_ws, stream=None)
+
+    def call(fn, base, **kw):
+        return fn(ctypes.byref(d), *{**base, **kw}.values())
+
+    for fn, base, needed in ((lib.deft_norm_forward, fwd, ("x", "gamma", "beta", "y", "mean", "rstd")),
+                             (lib.deft_norm_backward, bwd, ("x", "gamma", "beta", "mean", "rstd", "dy"))):
+        for k in needed:
+            assert call(fn, base, **{k: None}) == -4
+        for k in [k for k in base if k not in ("ws", "bytes", "stream")]:
+            assert call(fn, base, **{k: base[k] + 8}) == -7
+        assert call(fn, base, ws=None) == -5
+        assert call(fn, base, bytes=base["bytes"] - 1) == -5
+        assert call(fn, base, ws=FAKE + 4) == -7
+    size = 2 * 32 * 100000 * 2
+    assert call(lib.deft_norm_forward, fwd, y=FAKE) == -1
+    assert call(lib.deft_norm_forward, fwd, y=FAKE + size - 16) == -1
+    assert call(lib.deft_norm_backward, bwd, dx=FAKE) == -1
+    assert call(lib.deft_norm_backward, bwd, x=FAKE + far, dx=FAKE + 16) == -1
+
+
+def test_python_class_refuses():
+    with pytest.raises(ValueError):
+        GroupNormAct(1, 8, 4, 2, act="tanh", device="cpu")
+    with pytest.raises(ValueError):
+        GroupNormAct(1, 8, 4, 2, layout="nchw", device="cpu")
+    with pytest.raises(ValueError):
+        GroupNormAct(1, 8, 4, 2, dtype="f16", device="cpu")
+    with pytest.raises(L.DeftError):
+        GroupNormAct(1, 8, 4, 3, device="cpu")
+    h = GroupNormAct(2, 8, 4, 2, dtype="f32", device="cpu")
+    x, g = torch.zeros(2, 8, 4), torch.ones(8)
+    for bad in (dict(x=torch.zeros(2, 8, 5)), dict(x=torch.zeros(2, 4, 8).transpose(1, 2)), dict(x=x.bfloat16()),
+                dict(gamma=torch.ones(7)), dict(beta=g.double())):
+        a = {**dict(x=x, gamma=g, beta=g), **bad}
+        with pytest.raises(ValueError):
+            h.forward(a["x"], a["gamma"], a["beta"])
+    with pytest.raises(ValueError):
+        h.forward(x, g, g, y=torch.zeros(3))
+    with pytest.raises(ValueError):
+        h.forward(x, g, g, mean=torch.zeros(3))
+    st = torch.zeros(2, 2)
+    with pytest.raises(ValueError):
+        h.backward(x, g, g, st, st, x)
+    h = GroupNormAct(2, 8, 4, 2, dtype="f32", training=True, device="cpu")
+    with pytest.raises(ValueError):
+        h.backward(x, g, g, st, st[:1], x)
+    with pytest.raises(ValueError):
+        h.backward(x, g, g, st, st, x, out=dict(dx=None, dgamma=torch.zeros(2), dbeta=None))
+
+
+# ------------------------------------------------------------------ GPU
+
+def dev(a, layout, dtype):
+    """Channels-first float64 array -> device tensor of the layout, and its rounded values back."""
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(TYPES[dtype])
+    q = t.double().numpy()
+    if a.ndim == 3 and layout == "channels_last":
+        t = t.transpose(1, 2).contiguous()
+    return t.cuda(), q
+
+
+def host(t, layout):
+    t = t.detach().cpu().double()
+    return (t.transpose(1, 2) if t.dim() == 3 and layout == "channels_last" else t).numpy()
+
+
+def check(got, want, half, what):
+    value, bound = want
+    bound = bound + half * (np.abs(value) + bound) + 1e-37
+    bad = ~(np.abs(got - value) <= bound)
+    assert not bad.any(), "%s: %d of %d off, worst %.3g of its bound at %s" % (
+        what, bad.sum(), bad.size, np.nanmax(np.abs(got - value) / bound), np.argwhere(bad)[0])
+
+
+def inputs(n, c, s, layout, dtype, seed=0, offset=0.0):
+    r = np.random.default_rng(seed)
+    x = r.standard_normal((n, c, s)) * (0.5 + np.abs(r.standard_normal(c)))[:, None] + r.standard_normal(c)[:, None]
+    x, dy = dev(x + offset, layout, dtype), dev(r.standard_normal((n, c, s)), layout, dtype)
+    gamma = dev(1 + 0.3 * r.standard_normal(c), layout, dtype)
+    beta = dev(0.3 * r.standard_normal(c), layout, dtype)
+    return x, gamma, beta, dy
+
+
+def run_both(n, c, s, g, layout, dtype, name, eps=1e-5, seed=0, offset=0.0):
+    print("norm", n, c, s, g, layout, dtype, name, flush=True)
+    (x, xq), (gamma, gq), (beta, bq), (dy, dq) = inputs(n, c, s, layout, dtype, seed, offset)
+    h = GroupNormAct(n, c, s, g, eps=eps, act=name, layout=layout, dtype=dtype, training=True)
+    y, mean, rstd = h.forward(x, gamma, beta)
+    f = O.forward(xq, gq, bq, g, eps, name, dtype)
+    check(host(y, layout), f["y"], HALF[dtype], "y")
+    check(host(mean, layout), f["mean"], HALF["f32"], "mean")
+    check(host(rstd, layout), f["rstd"], HALF["f32"], "rstd")
+    out = h.backward(x, gamma, beta, mean, rstd, dy)
+    b = O.backward(xq, gq, bq, host(mean, layout), host(rstd, layout), dq, g, name, dtype)
+    for k in ("dx", "dgamma", "dbeta"):
+        check(host(out[k], layout), b[k], HALF[dtype], k)
+
+
+# (n, c, s, g): single elements, rows shorter than an access, ragged rows, channels that share an
+# access between groups, one channel a group, one group, groups of 2048 channels, groups that fit
+# one workgroup and groups that are cut, along rows, channels and positions
+SHAPES = [(1, 1, 1, 1), (2, 3, 1, 3), (1, 40, 1, 1), (3, 5, 7, 5), (2, 7, 33, 1), (2, 12, 3, 4), (2, 16, 256, 4),
+          (3, 36, 1000, 9), (1, 91, 129, 7), (2, 24, 50, 24), (1, 30, 515, 3), (2, 48, 784, 3), (1, 2048, 9, 1),
+          (1, 4096, 3, 2), (2, 320, 4099, 32), (1, 64, 20001, 1), (1, 3, 50001, 1), (1, 1, 70001, 1),
+          (1, 1500, 300, 4), (40, 256, 196, 32), (5, 8, 2047, 2)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda v: "x".join(map(str, v)))
+def test_against_the_oracle(shape, layout, dtype):
+    n, c, s, g = shape
+    run_both(n, c, s, g, layout, dtype, ACTS[(n + c + s + g) % 4])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_activations(name, layout, dtype):
+    run_both(2, 40, 301, 5, layout, dtype, name, seed=3)
+    run_both(1, 40, 6007, 5, layout, dtype, name, seed=4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("s", [50, 9001])
+def test_mean_far_from_zero(layout, s):
+    run_both(2, 24, s, 3, layout, "f32", "silu", seed=5, offset=1000.0)
+
+
+@pytest.mark.gpu
+def test_random_shapes():
+    r = np.random.default_rng(7)
+    for k in range(24):
+        per, g, n = int(r.integers(1, 41)), int(r.integers(1, 20)), int(r.integers(1, 6))
+        s = int(np.exp(r.uniform(0, math.log(max(2, 400000 // (per * g * n))))))
+        run_both(n, per * g, s, g, LAYOUTS[k % 2], ["f32", "bf16"][k // 2 % 2], ACTS[k // 4 % 4], seed=k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("s", [60, 30011])
+def test_constant_groups(layout, s):
+    """No variance: y = act(beta), and dx stays finite."""
+    n, c, g = 2, 16, 4
+    x, _ = dev(np.full((n, c, s), 3.0), layout, "f32")
+    gamma, _ = dev(np.linspace(0.5, 1.5, c), layout, "f32")
+    beta, bq = dev(np.linspace(-1, 1, c), layout, "f32")
+    h = GroupNormAct(n, c, s, g, act="relu", layout=layout, dtype="f32", training=True)
+    y, mean, rstd = h.forward(x, gamma, beta)
+    assert (mean == 3.0).all()
+    np.testing.assert_allclose(rstd.cpu().double().numpy(), 1e-5 ** -0.5, rtol=4 * 2.0 ** -24)
+    np.testing.assert_array_equal(host(y, layout), np.broadcast_to(np.maximum(bq, 0)[None, :, None], (n, c, s)))
+    out = h.backward(x, gamma, beta, mean, rstd, torch.ones_like(x))
+    assert all(torch.isfinite(v).all() for v in out.values())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("s", [60, 30011])
+def test_what_is_not_finite_stays_in_its_group(layout, s, name):
+    n, c, g = 2, 24, 3
+    (x, xq), (gamma, gq), (beta, bq), (dy, dq) = inputs(n, c, s, layout, "f32", seed=8)
+    h = GroupNormAct(n, c, s, g, act=name, layout=layout, dtype="f32", training=True)
+    y0, mean0, rstd0 = h.forward(x, gamma, beta)
+    d0 = h.backward(x, gamma, beta, mean0, rstd0, dy)
+    for bad in (math.nan, math.inf, -math.inf):
+        z = x.clone()
+        (z[1, :, 9] if layout == "channels_last" else z[1, 9])[s // 2] = bad  # image 1, group 1
+        y, mean, rstd = h.forward(z, gamma, beta)
+        other = np.ones((n, c), bool)
+        other[1, 8:16] = False
+        a, b = host(y, layout), host(y0, layout)
+        np.testing.assert_array_equal(a[other], b[other])
+        assert np.isnan(a[~other]).all()
+        d = h.backward(z, gamma, beta, mean, rstd, dy)
+        a, b = host(d["dx"], layout), host(d0["dx"], layout)
+        np.testing.assert_array_equal(a[other], b[other])
+        assert np.isnan(a[~other]).all()
+        np.testing.assert_array_equal(np.isnan(host(d["dgamma"], layout)), ~other[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("s", [100, 40003])
+def test_calls_repeat_their_bits_and_leave_out_what_is_not_wanted(layout, s):
+    n, c, g = 2, 40, 4
+    (x, _), (gamma, _), (beta, _), (dy, _) = inputs(n, c, s, layout, "bf16", seed=9)
+    h = GroupNormAct(n, c, s, g, act="gelu", layout=layout, training=True)
+    y, mean, rstd = h.forward(x, gamma, beta)
+    again = h.forward(x, gamma, beta)
+    for a, b in zip((y, mean, rstd), again):
+        assert torch.equal(a, b)
+    out = h.backward(x, gamma, beta, mean, rstd, dy)
+    for keep in (("dx",), ("dgamma", "dbeta"), ("dgamma",), ("dbeta",), ("dx", "dgamma", "dbeta"), ()):
+        part = h.backward(x, gamma, beta, mean, rstd, dy,
+                          out={k: torch.full_like(v, 7) if k in keep else None for k, v in out.items()})
+        for k in keep:
+            assert torch.equal(part[k], out[k]), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_writes_stay_inside_their_buffers(layout):
+    for n, c, s, g in ((1, 5, 9, 5), (2, 36, 101, 9), (1, 18, 20003, 2)):
+        (x, _), (gamma, _), (beta, _), (dy, _) = inputs(n, c, s, layout, "bf16", seed=10)
+        h = GroupNormAct(n, c, s, g, act="silu", layout=layout, training=True)
+
+        def guarded(like):
+            size = -(-like.numel() // 64) * 64
+            buf = torch.full((size + 128,), -7.0, dtype=like.dtype, device="cuda")
+            return buf, buf[64:64 + like.numel()].view(like.shape)
+
+        y0, mean, rstd = h.forward(x, gamma, beta)
+        d0 = h.backward(x, gamma, beta, mean, rstd, dy)
+        bufs = {k: guarded(v) for k, v in dict(y=y0, mean=mean, rstd=rstd, **d0).items()}
+        h.forward(x, gamma, beta, *(bufs[k][1] for k in ("y", "mean", "rstd")))
+        h.backward(x, gamma, beta, mean, rstd, dy, out={k: bufs[k][1] for k in d0})
+        for k, v in dict(y=y0, mean=mean, rstd=rstd, **d0).items():
+            buf, view = bufs[k]
+            assert torch.equal(view, v), k
+            assert (buf[:64] == -7).all() and (buf[64 + v.numel():] == -7).all(), k
+
+
+@pytest.mark.gpu
+def test_empty_calls():
+    for n, s in ((0, 5), (3, 0)):
+        h = GroupNormAct(n, 8, s, 2, dtype="f32", training=True)
+        x, g = torch.empty(n, 8, s, device="cuda"), torch.ones(8, device="cuda")
+        y, mean, rstd = h.forward(x, g, g)
+        assert y.shape == x.shape
+        out = h.backward(x, g, g, mean, rstd, x,
+                         out=dict(dx=torch.empty_like(x), dgamma=g.clone(), dbeta=g.clone()))
+        assert not out["dgamma"].any() and not out["dbeta"].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_side_stream_and_graph_replays(layout):
+    n, c, s, g = 2, 24, 20011, 3
+    (x, _), (gamma, _), (beta, _), (dy, _) = inputs(n, c, s, layout, "bf16", seed=11)
+    h = GroupNormAct(n, c, s, g, act="silu", layout=layout, training=True)
+
+    def step():
+        y, mean, rstd = h.forward(x, gamma, beta)
+        out = h.backward(x, gamma, beta, mean, rstd, dy)
+        return [y, mean, rstd, out["dx"], out["dgamma"], out["dbeta"]]
+
+    ref = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(other, ref):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(4):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, ref):
+            assert torch.equal(a, b)
+        x.mul_(0.5)
+        ref = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_offsets_past_32_bits(layout):
+    """Three images of 2^30 elements and more: the last one's result is that of the image alone."""
+    n, c, s, g = 3, 64, (1 << 24) + 3, 8
+    shape = (n, s, c) if layout == "channels_last" else (n, c, s)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    for k in range(n):
+        x[k].normal_(generator=gen)
+    gamma, beta = torch.ones(c, dtype=torch.bfloat16, device="cuda"), torch.zeros(c, dtype=torch.bfloat16, device="cuda")
+    all3 = GroupNormAct(n, c, s, g, act="relu", layout=layout, training=True)
+    one = GroupNormAct(1, c, s, g, act="relu", layout=layout, training=True)
+    y, mean, rstd = all3.forward(x, gamma, beta)
+    dx = all3.backward(x, gamma, beta, mean, rstd, y, out=dict(dx=torch.empty_like(x), dgamma=None, dbeta=None))["dx"]
+    for k in (0, 2):
+        y1, mean1, rstd1 = one.forward(x[k:k + 1], gamma, beta)
+        assert torch.equal(mean[k], mean1[0]) and torch.equal(rstd[k], rstd1[0])
+        assert torch.equal(y[k], y1[0])
+        dx1 = one.backward(x[k:k + 1], gamma, beta, mean1, rstd1, y1,
+                           out=dict(dx=torch.empty_like(y1), dgamma=None, dbeta=None))["dx"]
+        assert torch.equal(dx[k], dx1[0])
+        # 2^27 standard normal numbers a group: 6 standard deviations
+        assert mean1.abs().max() < 6 * 2.0 ** -13.5 and (rstd1 - 1).abs().max() < 6 * 2.0 ** -14 + 1e-4
