@@ -310,9 +310,16 @@ typedef struct deft_norm_desc {
 /* DEFT_OK, or the code with which the calls below refuse the descriptor. */
 int deft_norm_desc_validate(const deft_norm_desc* d);
 
-/* Workspace bytes of deft_norm_forward (training = 0) or deft_norm_backward
- * (training = 1); 0 for a descriptor that they refuse. */
+/* Bytes of a workspace for deft_norm_forward (training = 0), or for it and
+ * deft_norm_backward (training = 1); 0 for a descriptor that they refuse.
+ * Zero a workspace before its first call, use it for one descriptor, and order
+ * the calls on it: workgroups that share a group count their calls in it. */
 size_t deft_norm_workspace_bytes(const deft_norm_desc* d, int training);
+
+/* How long (ticks of 10 ns; 2 ms at first) a workgroup of either call waits
+ * for the others that share its group, before it computes their sums itself;
+ * the results are the same.  For tests; holds for all later calls. */
+void deft_debug_norm_patience(uint32_t ticks);
 
 /* y = act(group norm of x), and mean and rstd (fp32 [n][groups], written) as
  * deft_norm_backward takes them.  y must not overlap x.  n = 0 or s = 0 is a

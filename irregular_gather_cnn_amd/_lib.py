@@ -30,7 +30,7 @@ EXPORTED = ["deft_desc_validate", "deft_plan_create", "deft_plan_create_forced",
             "deft_timing_get", "deft_dwconv1d_forward", "deft_dwpw1d_forward",
             "deft_adamw_step", "deft_grad_norm", "deft_grad_norm_workspace_bytes",
             "deft_norm_desc_validate", "deft_norm_workspace_bytes", "deft_norm_forward",
-            "deft_norm_backward"]
+            "deft_norm_backward", "deft_debug_norm_patience"]
 LAYOUTS = {"channels_first": 0, "channels_last": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
@@ -115,6 +115,7 @@ def load() -> ctypes.CDLL:
         "deft_grad_norm_workspace_bytes": (sz, [i]),
         "deft_norm_desc_validate": (i, [ctypes.POINTER(deft_norm_desc)]),
         "deft_norm_workspace_bytes": (sz, [ctypes.POINTER(deft_norm_desc), i]),
+        "deft_debug_norm_patience": (None, [ctypes.c_uint32]),
         "deft_norm_forward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 7 + [sz, vp]),
         "deft_norm_backward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 10 + [sz, vp]),
         "deft_error_string": (ctypes.c_char_p, [i]),
@@ -133,12 +134,12 @@ def load() -> ctypes.CDLL:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None or isinstance(t, int):
+        return t
     if isinstance(t, ctypes.c_void_p):
         return t.value
     raise TypeError("expected a tensor, int or None, got %r" % type(t))
@@ -275,6 +276,10 @@ def deft_norm_desc_validate(desc: deft_norm_desc) -> None:
 
 def deft_norm_workspace_bytes(desc: deft_norm_desc, training: int) -> int:
     return int(load().deft_norm_workspace_bytes(ctypes.byref(desc), int(training)))
+
+
+def deft_debug_norm_patience(ticks: int) -> None:
+    load().deft_debug_norm_patience(int(ticks))
 
 
 def deft_norm_forward(desc: deft_norm_desc, x, gamma, beta, y, mean, rstd, workspace, ws_bytes, stream=None) -> None:

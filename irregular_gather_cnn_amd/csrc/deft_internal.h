@@ -173,11 +173,12 @@ hipError_t launch_grad_norm(const double* partials, int count, double max_norm, 
 
 // Group norm with activation (deft_norm_fwd.hip, deft_norm_bwd.hip).  A group
 // of an image, or a band of whole groups where channels come last, is cut into
-// `slices` that one workgroup each holds in registers.  One slice: statistics
-// and result in one launch.  More: partial statistics, their combination, and
-// the result from a second read.
+// `slices` that one workgroup each holds in registers.  One slice, or several
+// that the chip holds at once: statistics and result in one launch, in which
+// the slices' workgroups join their sums.  More: partial statistics, their
+// combination, and the result from a second read.
 constexpr int kNormThreads = 512;
-enum NormMode { kNormWhole = 0, kNormStats = 1, kNormApply = 2 };
+enum NormMode { kNormWhole = 0, kNormJoint = 1, kNormStats = 2, kNormApply = 3 };
 struct NormArgs {
   const void* x;
   const void* dy;     // backward
@@ -188,12 +189,21 @@ struct NormArgs {
   float* rstd;
   float* part;        // partial sums, one block per slice: see each kernel
   float* sums;        // backward, several slices: [n][g][2] sums of gamma dz and of gamma dz h
+  void* dgamma;       // backward, nullable; written by the main kernel where `arrivals` is set
+  void* dbeta;
+  uint64_t* arrivals; // [bands or groups]: workgroups that have written their sums, over all calls
   int n, c, s, g, per, act;
   float eps;
   int slices, rp;     // channels last: rows (positions) per slice; first: channels per slice
   int bands;          // channels last
   int ws, cp;         // channels first: slices along the positions, and positions in each
   int lt;             // channels first: log2 of the lanes that share a channel's positions
+  // joint: per cluster a call counter, words of each slice and group, totals of each group
+  uint64_t* counter;
+  uint64_t* words;
+  uint64_t* totals;
+  int direct;         // every workgroup reads every slice's words; else totals are made and read
+  uint32_t patience;  // ticks (10 ns) that a workgroup waits for its peers
 };
 struct NormPlan {     // how a call is cut
   int vec, u, threads;  // elements per access, accesses per thread, threads per workgroup

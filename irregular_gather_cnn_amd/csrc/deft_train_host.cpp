@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -27,9 +28,8 @@ int norm_launches(int count) { return std::max(1, (count + deft::kNormList - 1) 
 
 // ---- group norm: how a call is cut ----
 
-constexpr int kMaxU = 16;          // accesses per thread of the widest kernels
 constexpr int kMaxPer = 2048;      // channels per group: a row of one group fits a workgroup
-constexpr uint64_t kFill = 512;    // workgroups that fill the chip, two on each compute unit
+constexpr int kCus = 256;
 constexpr size_t kAlign = 256;
 
 size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
@@ -51,38 +51,81 @@ int norm_desc_status(const deft_norm_desc* d) {
 struct NormCut {
   deft::NormArgs a;
   deft::NormPlan p;
-  bool whole;
+  int mode;  // kNormWhole, kNormJoint, or kNormStats: statistics, then a second launch
 };
 
-// Channels last.  One slice where a band of whole groups, 128 bytes of each
-// row or more, fits the registers; else slices of whole rows (of 1024 channels
-// at most), as many as fill the chip.
+// Workgroups of `threads` that the chip holds at once: the forward's joint
+// kernels take up to 128 registers, the backward's up to 256.
+int resident(bool back, int threads) { return kCus * (back ? 512 : 1024) / threads; }
+
+// One slice for a group (or a band of groups), where it fits the registers:
+// 32 accesses a thread forward, 16 of x and of dy backward.  It needs no
+// exchange, which costs 4 to 5 us, but only as many compute units work as there
+// are groups; so where these leave units idle, it pays up to about 3 us of one
+// unit's vector operations.  Measured forward (gelu, fp32, us in one slice and
+// joined): 27 groups of 4000 elements 8.6 and 10.5; 2x14 groups of 12136 18.7
+// and 10.9; 25 groups of 31878 19.3 and 13.8.
+bool whole_pays(const deft_norm_desc& d, bool back, int V, int rounds, int64_t units, int64_t elems) {
+  if (rounds > (V == 1 || back ? 16 : 32)) return false;
+  if (units >= kCus * 3 / 4) return true;
+  const int ops = (d.act == DEFT_ACT_GELU ? 40 : d.act == DEFT_ACT_SILU ? 24 : 12) * (back ? 2 : 1);
+  return elems * ops <= (back ? 600000 : 400000);
+}
+
+// Channels last.  Whole: bands of groups, 32 bytes of each row or more (64
+// backward from 2^20 elements on, where the lines that bands share no longer
+// come from the cache: 16x784x512 bf16 takes 20 us against 24).  Else slices of
+// whole rows, of 1024 channels at most, of 4 to 8 accesses a thread (fewer when
+// they would leave compute units idle: 443 slices of 4 rows took 18 us where 111
+// of 16 take 14).
 void cut_last(const deft_norm_desc& d, bool back, NormCut& r) {
-  const int nt = deft::kNormThreads, per = r.a.per, g = d.groups, esz = elem_size(d.dtype);
+  const int per = r.a.per, g = d.groups, esz = elem_size(d.dtype);
   const int V = d.c >= 16 / esz ? 16 / esz : 1;
   r.p.vec = V;
-  r.p.threads = nt;
   // chunks across the widest of `bands` bands
   auto widest = [&](int bands) { return ceil_div((int64_t)ceil_div(g, bands) * per, V); };
-  int bands = std::max(1, g / std::min(g, ceil_div(128, per * esz)));
+  int nt = deft::kNormThreads;
+  const int wide = back && (int64_t)d.n * d.s * d.c >= 1 << 20 ? 64 : 32;
+  int bands = std::max(1, g / std::min(g, ceil_div(wide, per * esz)));
+  while (bands > 1 && g / bands * per < V) --bands;
   int rounds = ceil_div(d.s, nt / widest(bands));
-  r.whole = rounds <= kMaxU && (rounds <= 4 || (uint64_t)d.n * bands >= kFill / 4);
+  r.mode = deft::kNormWhole;
   r.a.slices = 1;
   r.a.rp = d.s;
-  if (!r.whole) {
+  if (!whole_pays(d, back, V, rounds, (int64_t)d.n * bands, (int64_t)ceil_div(g, bands) * per * d.s)) {
     bands = ceil_div(g, std::max(1, 1024 / per));
-    const int ty = nt / widest(bands);
+    nt = back && widest(bands) <= 256 ? 256 : deft::kNormThreads;
+    int ty = nt / widest(bands);
     rounds = 8;
-    while (rounds > 1 && (uint64_t)d.n * bands * ceil_div(d.s, (int64_t)ty * rounds) < kFill) rounds /= 2;
+    auto slices = [&] { return ceil_div(d.s, (int64_t)ty * rounds); };
+    while (rounds > 4 && (int64_t)d.n * bands * slices() < kCus) rounds /= 2;
+    if (back && slices() > resident(back, nt)) {  // the largest slices there are
+      nt = deft::kNormThreads;
+      ty = nt / widest(bands);
+      rounds = 16;
+    }
+    r.mode = slices() <= resident(back, nt) ? deft::kNormJoint : deft::kNormStats;
     r.a.rp = ty * rounds;
+    if (back && r.mode == deft::kNormStats) {
+      // read twice: small accumulating workgroups, four on each unit, whose slices'
+      // sums are few; no slice over 64 accesses, to keep the chains of sums short
+      nt = widest(bands) <= 256 ? 256 : deft::kNormThreads;
+      ty = nt / widest(bands);
+      rounds = 4;
+      const int blocks = ceil_div(d.s, ty * rounds), want = std::max(1, 4 * kCus / std::max(1, d.n * bands));
+      r.a.rp = std::min(ceil_div(blocks, std::min(blocks, want)), 16) * ty * rounds;
+    }
     r.a.slices = ceil_div(d.s, r.a.rp);
+    // with more words than this it takes a workgroup longer to read them all than to
+    // wait until others have added them up
+    r.a.direct = r.a.slices * ceil_div(g, bands) <= 2048;
   }
   r.a.bands = bands;
   r.p.u = rounds;
-  const int cols = ceil_div(g, bands) * per, ng = ceil_div(g, bands);
-  // thread rows and odd pitch: at most nt * V elements and one more per row
-  const size_t red = (size_t)nt * V + nt;
-  r.p.lds = sizeof(float) * (back ? 2 * red + 2 * (size_t)cols + 2 * (size_t)ng : red + 2 * (size_t)ng);
+  r.p.threads = nt;
+  const size_t cols = (size_t)ceil_div(g, bands) * per, ng = ceil_div(g, bands);
+  // two matrices of thread rows and odd pitch: at most nt * V elements and one more per row
+  r.p.lds = sizeof(float) * (2 * ((size_t)nt * V + nt) + (back ? 4 : 2) * (ng + cols));
 }
 
 // Accesses per thread of `rows` channels with `chunks` chunks each, and the
@@ -100,8 +143,9 @@ int best_team(int nt, int rows, int chunks, int* lt) {
   return best;
 }
 
-// Channels first.  One slice where a group fits the registers; else slices of
-// whole channels, or of a channel's positions where one is long.
+// Channels first.  Whole: one workgroup a group, no larger than four accesses a
+// thread need.  Else slices of whole channels, or of a channel's positions where
+// one is long, of 4 to 8 accesses a thread.
 void cut_first(const deft_norm_desc& d, bool back, NormCut& r) {
   const int per = r.a.per, esz = elem_size(d.dtype), V = d.s >= 16 / esz ? 16 / esz : 1;
   const int chunks = ceil_div(d.s, V);
@@ -109,29 +153,31 @@ void cut_first(const deft_norm_desc& d, bool back, NormCut& r) {
   int nt = 64;
   int rounds = best_team(nt, per, chunks, &r.a.lt);
   while (rounds > 4 && nt < deft::kNormThreads) rounds = best_team(nt *= 2, per, chunks, &r.a.lt);
-  r.whole = rounds <= kMaxU && (rounds <= 4 || (uint64_t)d.n * d.groups >= kFill / 4);
+  r.mode = deft::kNormWhole;
   r.a.rp = per;
   r.a.ws = 1;
   r.a.cp = d.s;
-  if (!r.whole) {
-    nt = deft::kNormThreads;
-    int cpc = ceil_div(chunks, ceil_div(chunks, 4 * nt));  // chunks of a channel in a slice
-    int rp = std::min(per, std::max(1, 8 * nt / cpc));
-    auto slices = [&] { return (uint64_t)ceil_div(per, rp) * ceil_div(chunks, cpc); };
-    while ((uint64_t)d.n * d.groups * slices() < kFill && rp * (int64_t)cpc > nt) {
+  if (!whole_pays(d, back, V, rounds, (int64_t)d.n * d.groups, (int64_t)per * d.s)) {
+    nt = back ? 256 : deft::kNormThreads;
+    int cpc = ceil_div(chunks, ceil_div(chunks, nt * 4));  // chunks of a channel in a slice
+    int rp = std::min(per, std::max(1, nt * 8 / cpc));
+    auto slices = [&] { return (int64_t)ceil_div(per, rp) * ceil_div(chunks, cpc); };
+    while ((int64_t)d.n * d.groups * slices() < kCus && rp * (int64_t)cpc > nt * 4) {
       if (rp > 1) rp = (rp + 1) / 2;
       else cpc = (cpc + 1) / 2;
     }
-    while ((rounds = best_team(nt, rp, cpc, &r.a.lt)) > kMaxU) --rp;  // rp = 1: four at most
+    while ((rounds = best_team(nt, rp, cpc, &r.a.lt)) > 8) --rp;  // rp = 1: four at most
     r.a.rp = rp;
     r.a.cp = cpc * V;
     r.a.ws = ceil_div(chunks, cpc);
+    r.mode = slices() <= resident(back, nt) ? deft::kNormJoint : deft::kNormStats;
+    r.a.direct = 1;
   }
   r.a.slices = ceil_div(per, r.a.rp) * r.a.ws;
   r.p.threads = nt;
   r.p.u = rounds;
   const int subs = std::max(1, (1 << r.a.lt) >> 6);
-  r.p.lds = sizeof(float) * (back ? 16 + (2 + 2 * (size_t)subs) * r.a.rp : 8 + 2 * (size_t)r.a.rp);
+  r.p.lds = sizeof(float) * (back ? std::max(2 * nt, 16 + (2 + 2 * subs) * r.a.rp) : 32 + 2 * r.a.rp);
 }
 
 int norm_cut(const deft_norm_desc& d, bool back, NormCut& r) {
@@ -153,14 +199,38 @@ int norm_cut(const deft_norm_desc& d, bool back, NormCut& r) {
 int norm_parts(const deft_norm_desc& d, const NormCut& r) {
   return d.layout == DEFT_CHANNELS_LAST ? r.a.slices : r.a.ws;
 }
-size_t norm_part_bytes(const deft_norm_desc& d, const NormCut& r, bool back) {
-  if (back) return round_up((size_t)d.n * norm_parts(d, r) * 2 * d.c * sizeof(float), kAlign);
-  return r.whole ? 0 : (size_t)d.n * d.groups * r.a.slices * 2 * sizeof(float);
+
+// One direction's share of a workspace, at `base`: what joint workgroups share
+// (kept from call to call), then the partial sums.  Fills in the pointers and
+// returns the bytes.
+size_t norm_layout(const deft_norm_desc& d, bool back, NormCut& r, char* base) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base + at;
+    at = round_up(at + bytes, kAlign);
+    return p;
+  };
+  const size_t groups = (size_t)d.n * d.groups;
+  if (r.mode == deft::kNormJoint) {
+    const size_t clusters = d.layout == DEFT_CHANNELS_LAST ? (size_t)d.n * r.a.bands : groups;
+    r.a.counter = (uint64_t*)take(clusters * 8);
+    r.a.words = (uint64_t*)take(groups * r.a.slices * 16);
+    r.a.totals = (uint64_t*)take(r.a.direct ? 0 : groups * 16);
+  }
+  // Small calls: the last workgroup sums up dgamma and dbeta.  That saves a launch
+  // (3 us on the host), and costs 1 to 3 us on the device, which has time here.
+  if (back && r.mode == deft::kNormWhole && (int64_t)d.n * d.s * d.c <= 200000)
+    r.a.arrivals = (uint64_t*)take((d.layout == DEFT_CHANNELS_LAST ? r.a.bands : d.groups) * 8);
+  if (back) {
+    r.a.part = (float*)take((size_t)d.n * norm_parts(d, r) * 2 * d.c * 4);
+    r.a.sums = (float*)take(r.mode == deft::kNormStats ? groups * 8 : 0);
+  } else {
+    r.a.part = (float*)take(r.mode == deft::kNormStats ? groups * r.a.slices * 8 : 0);
+  }
+  return at;
 }
-size_t norm_ws_bytes(const deft_norm_desc& d, const NormCut& r, bool back) {
-  const size_t sums = back && !r.whole ? (size_t)d.n * d.groups * 2 * sizeof(float) : 0;
-  return round_up(norm_part_bytes(d, r, back) + sums, kAlign);
-}
+
+std::atomic<uint32_t> g_patience{200000};  // 2 ms
 
 bool overlap(const void* a, const void* b, size_t bytes) {
   const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
@@ -288,10 +358,14 @@ int deft_norm_desc_validate(const deft_norm_desc* d) {
 }
 
 size_t deft_norm_workspace_bytes(const deft_norm_desc* d, int training) {
-  NormCut r;
-  if (norm_desc_status(d) != DEFT_OK || d->n == 0 || d->s == 0 || norm_cut(*d, training != 0, r) != DEFT_OK) return 0;
-  return norm_ws_bytes(*d, r, training != 0);
+  NormCut f, b;
+  if (norm_desc_status(d) != DEFT_OK || d->n == 0 || d->s == 0 || norm_cut(*d, false, f) != DEFT_OK) return 0;
+  const size_t fwd = norm_layout(*d, false, f, nullptr);
+  if (!training) return fwd;
+  return norm_cut(*d, true, b) == DEFT_OK ? fwd + norm_layout(*d, true, b, nullptr) : 0;
 }
+
+void deft_debug_norm_patience(uint32_t ticks) { g_patience = ticks; }
 
 int deft_norm_forward(const deft_norm_desc* d, const void* x, const void* gamma, const void* beta, void* y,
                       float* mean, float* rstd, void* workspace, size_t ws_bytes, void* stream) {
@@ -305,17 +379,18 @@ int deft_norm_forward(const deft_norm_desc* d, const void* x, const void* gamma,
       !aligned16(rstd))
     return DEFT_ERR_ALIGN;
   if (overlap(x, y, (size_t)d->n * d->s * d->c * elem_size(d->dtype))) return DEFT_ERR_BAD_DESC;
-  const size_t need = norm_ws_bytes(*d, r, false);
+  const size_t need = norm_layout(*d, false, r, (char*)workspace);
   if (need && (!workspace || ws_bytes < need)) return DEFT_ERR_WORKSPACE;
   if (need && !aligned16(workspace)) return DEFT_ERR_ALIGN;
   r.a.x = x; r.a.gamma = gamma; r.a.beta = beta; r.a.out = y;
   r.a.mean = mean; r.a.rstd = rstd;
-  r.a.part = (float*)workspace;
+  r.a.patience = g_patience;
   const hipStream_t s = (hipStream_t)stream;
-  if (r.whole) return status_of(deft::launch_norm_fwd(r.a, r.p, d->layout, d->dtype, deft::kNormWhole, s));
-  hipError_t e = deft::launch_norm_fwd(r.a, r.p, d->layout, d->dtype, deft::kNormStats, s);
-  if (e == hipSuccess) e = deft::launch_norm_combine(r.a, d->layout, s);
-  if (e == hipSuccess) e = deft::launch_norm_fwd(r.a, r.p, d->layout, d->dtype, deft::kNormApply, s);
+  hipError_t e = deft::launch_norm_fwd(r.a, r.p, d->layout, d->dtype, r.mode, s);
+  if (r.mode == deft::kNormStats) {
+    if (e == hipSuccess) e = deft::launch_norm_combine(r.a, d->layout, s);
+    if (e == hipSuccess) e = deft::launch_norm_fwd(r.a, r.p, d->layout, d->dtype, deft::kNormApply, s);
+  }
   return status_of(e);
 }
 
@@ -329,30 +404,31 @@ int deft_norm_backward(const deft_norm_desc* d, const void* x, const void* gamma
   const bool params = dgamma || dbeta;
   if (d->n == 0 || d->s == 0)
     return params ? status_of(deft::launch_norm_params(nullptr, 0, d->c, dgamma, dbeta, d->dtype, s)) : DEFT_OK;
-  NormCut r;
-  if ((st = norm_cut(*d, true, r)) != DEFT_OK) return st;
+  NormCut f, r;
+  if ((st = norm_cut(*d, false, f)) != DEFT_OK || (st = norm_cut(*d, true, r)) != DEFT_OK) return st;
   if (!x || !gamma || !beta || !mean || !rstd || !dy) return DEFT_ERR_NULLPTR;
   if (!aligned16(x) || !aligned16(gamma) || !aligned16(beta) || !aligned16(mean) || !aligned16(rstd) ||
       !aligned16(dy))
     return DEFT_ERR_ALIGN;
   const size_t bytes = (size_t)d->n * d->s * d->c * elem_size(d->dtype);
   if (overlap(dx, x, bytes) || overlap(dx, dy, bytes)) return DEFT_ERR_BAD_DESC;
-  if (!workspace || ws_bytes < norm_ws_bytes(*d, r, true)) return DEFT_ERR_WORKSPACE;
+  // the forward's share comes first
+  const size_t fwd = norm_layout(*d, false, f, (char*)workspace);
+  if (!workspace || ws_bytes < fwd + norm_layout(*d, true, r, (char*)workspace + fwd)) return DEFT_ERR_WORKSPACE;
   if (!aligned16(workspace)) return DEFT_ERR_ALIGN;
   if (!dx && !params) return DEFT_OK;
   r.a.x = x; r.a.gamma = gamma; r.a.beta = beta; r.a.dy = dy; r.a.out = dx;
   r.a.mean = const_cast<float*>(mean); r.a.rstd = const_cast<float*>(rstd);  // only read
-  r.a.part = (float*)workspace;
-  r.a.sums = (float*)((char*)workspace + norm_part_bytes(*d, r, true));
-  hipError_t e;
-  if (r.whole) {
-    e = deft::launch_norm_bwd(r.a, r.p, d->layout, d->dtype, deft::kNormWhole, s);
-  } else {
-    e = deft::launch_norm_bwd(r.a, r.p, d->layout, d->dtype, deft::kNormStats, s);
-    if (e == hipSuccess && dx) e = deft::launch_norm_bwd_sums(r.a, d->layout, d->dtype, s);
-    if (e == hipSuccess && dx) e = deft::launch_norm_bwd(r.a, r.p, d->layout, d->dtype, deft::kNormApply, s);
+  r.a.patience = g_patience;
+  const bool after = params && !r.a.arrivals;
+  if (!params) r.a.arrivals = nullptr;
+  r.a.dgamma = dgamma; r.a.dbeta = dbeta;
+  hipError_t e = deft::launch_norm_bwd(r.a, r.p, d->layout, d->dtype, r.mode, s);
+  if (r.mode == deft::kNormStats && dx) {
+    if (e == hipSuccess) e = deft::launch_norm_bwd_sums(r.a, d->layout, d->dtype, s);
+    if (e == hipSuccess) e = deft::launch_norm_bwd(r.a, r.p, d->layout, d->dtype, deft::kNormApply, s);
   }
-  if (e == hipSuccess && params)
+  if (e == hipSuccess && after)
     e = deft::launch_norm_params(r.a.part, d->n * norm_parts(*d, r), d->c, dgamma, dbeta, d->dtype, s);
   return status_of(e);
 }

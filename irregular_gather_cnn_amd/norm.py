@@ -9,6 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
+from ._stream import current_stream
 
 
 class GroupNormAct:
@@ -35,37 +36,39 @@ class GroupNormAct:
                                         _lib.DEFT_BF16 if dtype == "bf16" else _lib.DEFT_F32, eps)
         _lib.deft_norm_desc_validate(self.desc)
         self.n, self.c, self.s, self.groups = n, c, s, groups
-        self.tdtype, self.device, self.training = _DTYPES[dtype], torch.device(device), training
-        self.ws_bytes = max(_lib.deft_norm_workspace_bytes(self.desc, k) for k in range(2 if training else 1))
-        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
+        self.tdtype, self.training = _DTYPES[dtype], training
+        self.ws_bytes = _lib.deft_norm_workspace_bytes(self.desc, 1 if training else 0)
+        self.ws = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
+        self.device = self.ws.device
+        self._index = self.ws.get_device()
+        self._stats = torch.empty((n, groups), dtype=torch.float32, device=device)
+        image, channel, stat = (n * c * s, self.tdtype), (c, self.tdtype), (n * groups, torch.float32)
+        self._kinds = dict(x=image, y=image, dy=image, dx=image, gamma=channel, beta=channel, dgamma=channel,
+                           dbeta=channel, mean=stat, rstd=stat)
 
-    def _take(self, what, t, size, dtype):
-        if t.numel() != size or t.dtype != dtype or t.device.type != self.device.type or not t.is_contiguous():
-            raise ValueError("%s must be %d contiguous elements of %s on %s" % (what, size, dtype, self.device))
-
-    def _take_inputs(self, x, gamma, beta):
-        self._take("x", x, self.n * self.c * self.s, self.tdtype)
-        self._take("gamma", gamma, self.c, self.tdtype)
-        self._take("beta", beta, self.c, self.tdtype)
+    def _check(self, **tensors):
+        for what, t in tensors.items():
+            size, dtype = self._kinds[what]
+            if t.numel() != size or t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous():
+                raise ValueError("%s must be %d contiguous elements of %s on %s" % (what, size, dtype, self.device))
 
     def forward(self, x, gamma, beta, y=None, mean=None, rstd=None):
         """(y, mean, rstd); mean and rstd are float32 [n][groups]."""
-        self._take_inputs(x, gamma, beta)
-        stats = self.n * self.groups
+        self._check(x=x, gamma=gamma, beta=beta)
         if y is None:
             y = torch.empty_like(x)
         else:
-            self._take("y", y, x.numel(), self.tdtype)
+            self._check(y=y)
         if mean is None:
-            mean = torch.empty((self.n, self.groups), dtype=torch.float32, device=x.device)
+            mean = torch.empty_like(self._stats)
         else:
-            self._take("mean", mean, stats, torch.float32)
+            self._check(mean=mean)
         if rstd is None:
-            rstd = torch.empty((self.n, self.groups), dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(self._stats)
         else:
-            self._take("rstd", rstd, stats, torch.float32)
+            self._check(rstd=rstd)
         _lib.deft_norm_forward(self.desc, x, gamma, beta, y, mean, rstd, self.ws, self.ws_bytes,
-                               torch.cuda.current_stream(x.device).cuda_stream)
+                               current_stream(self.device))
         return y, mean, rstd
 
     def backward(self, x, gamma, beta, mean, rstd, dy, out=None):
@@ -73,18 +76,13 @@ class GroupNormAct:
         holds as None is not computed."""
         if not self.training:
             raise ValueError("backward needs training=True")
-        self._take_inputs(x, gamma, beta)
-        self._take("dy", dy, x.numel(), self.tdtype)
-        for what, t in (("mean", mean), ("rstd", rstd)):
-            self._take(what, t, self.n * self.groups, torch.float32)
+        self._check(x=x, gamma=gamma, beta=beta, mean=mean, rstd=rstd, dy=dy)
         if out is None:
             out = dict(dx=torch.empty_like(x), dgamma=torch.empty_like(gamma), dbeta=torch.empty_like(beta))
         else:
-            for what, like in (("dx", x), ("dgamma", gamma), ("dbeta", beta)):
-                if out[what] is not None:
-                    self._take(what, out[what], like.numel(), self.tdtype)
+            self._check(**{k: t for k, t in out.items() if t is not None})
         _lib.deft_norm_backward(self.desc, x, gamma, beta, mean, rstd, dy, out["dx"], out["dgamma"], out["dbeta"],
-                                self.ws, self.ws_bytes, torch.cuda.current_stream(x.device).cuda_stream)
+                                self.ws, self.ws_bytes, current_stream(self.device))
         return out
 
 

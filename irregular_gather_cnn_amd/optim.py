@@ -11,6 +11,7 @@ import ctypes
 import torch
 
 from . import _lib
+from ._stream import current_stream
 
 _DTYPES = {torch.float32: _lib.DEFT_F32, torch.bfloat16: _lib.DEFT_BF16}
 
@@ -28,10 +29,6 @@ def _dense(t, what, device=None):
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, not on %s" % (what, t.device, device))
     return t
-
-
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 class _Gradients:
@@ -87,7 +84,7 @@ class GradNorm:
     def __call__(self, max_norm=float("inf"), inv_scale=1.0):
         g = self.grads
         _lib.deft_grad_norm(g.pointers, self._n, len(g.sizes), g.dtype, max_norm, inv_scale, self.control, self.ws,
-                            self.ws_bytes, _stream(g.device))
+                            self.ws_bytes, current_stream(g.device))
         return self.control
 
 
@@ -191,5 +188,5 @@ class AdamW:
                 raise ValueError("%s must be %d contiguous elements of %s on %s" % (what, n, kind, self.device))
         d = self._desc
         d.lr, d.step, d.seed = self.lr, self.steps + 1, self.step_seed(self.steps + 1)
-        _lib.deft_adamw_step(d, self._list, len(self.params), control, schedule, _stream(self.device))
+        _lib.deft_adamw_step(d, self._list, len(self.params), control, schedule, current_stream(self.device))
         self.steps += 1

@@ -409,3 +409,38 @@ def test_offsets_past_32_bits(layout):
         assert torch.equal(dx[k], dx1[0])
         # 2^27 standard normal numbers a group: 6 standard deviations
         assert mean1.abs().max() < 6 * 2.0 ** -13.5 and (rstd1 - 1).abs().max() < 6 * 2.0 ** -14 + 1e-4
+
+
+@pytest.fixture
+def no_patience():
+    L.deft_debug_norm_patience(0)
+    yield
+    L.deft_debug_norm_patience(200000)
+
+
+# groups that several workgroups hold: few and many slices, along rows, channels and positions, and
+# words that each workgroup reads or that are first summed up
+JOINT = [(2, 320, 4099, 32), (1, 64, 20001, 1), (1, 3, 50001, 1), (3, 96, 9000, 48), (1, 512, 3000, 2),
+         (2, 1920, 700, 480)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("shape", JOINT, ids=lambda v: "x".join(map(str, v)))
+def test_workgroups_that_do_not_wait_give_the_same_bits(shape, layout, dtype, request):
+    n, c, s, g = shape
+    print("joint", shape, layout, dtype, flush=True)
+    run_both(n, c, s, g, layout, dtype, "silu", seed=12)
+    (x, _), (gamma, _), (beta, _), (dy, _) = inputs(n, c, s, layout, dtype, seed=12)
+    h = GroupNormAct(n, c, s, g, act="silu", layout=layout, dtype=dtype, training=True)
+    y, mean, rstd = h.forward(x, gamma, beta)
+    d = h.backward(x, gamma, beta, mean, rstd, dy)
+    request.getfixturevalue("no_patience")
+    for _ in range(3):
+        again = h.forward(x, gamma, beta)
+        for a, b in zip(again, (y, mean, rstd)):
+            assert torch.equal(a, b)
+        again = h.backward(x, gamma, beta, mean, rstd, dy)
+        for k in d:
+            assert torch.equal(again[k], d[k]), k
