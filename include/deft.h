@@ -417,7 +417,9 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
 int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtype, double max_norm,
                    double inv_scale, float* control, void* workspace, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of deft_grad_norm for a list of `count` tensors. */
+/* Workspace bytes of deft_grad_norm for a list of `count` tensors.  Zero a
+ * workspace before its first call, and order the calls on it: its workgroups
+ * count themselves in it. */
 size_t deft_grad_norm_workspace_bytes(int count);
 
 /* Per-kernel timing for benchmarks (host-side events only; no device memory).

@@ -130,7 +130,7 @@ hipError_t launch_backward(const deft_plan& p, const BackwardArgs& a, hipStream_
 // to the device and can be captured; longer lists take several launches.
 constexpr int kStateBlock = DEFT_STATE_BLOCK;  // elements per scale of an 8-bit state
 constexpr int kAdamwElems = 4 * kStateBlock;   // per workgroup
-constexpr int kAdamwList = 40, kNormList = 64; // tensors per launch
+constexpr int kAdamwList = 50, kNormList = 64; // tensors per launch
 struct AdamwTensor {
   void* p;
   const void* g;
@@ -140,13 +140,12 @@ struct AdamwTensor {
   float* v_scale;
   float* master;
   int64_t n;
-  double wd;
-  float decay;  // 1 - lr wd
-  uint32_t id;  // number in the call's list
+  double decay;    // 1 - lr wd, to be rounded to fp32; wd where the schedule has lr
 };
 struct AdamwArgs {
   AdamwTensor t[kAdamwList];
   uint32_t first[kAdamwList];  // first workgroup of each tensor
+  uint32_t id[kAdamwList];     // its number in the call's list
   int count;
   float b1, c1, b2, c2, eps, rate, low;
   uint32_t seed;
@@ -156,20 +155,23 @@ struct AdamwArgs {
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
 hipError_t launch_adamw(const AdamwArgs& a, uint32_t blocks, int p_dtype, int g_dtype, int bits, bool master,
                         hipStream_t st);
-constexpr int kNormPiece = 8192;      // elements a workgroup sums at a time
-constexpr uint32_t kNormGrid = 1024;  // workgroups, and partial sums, per launch
+constexpr int kSquareThreads = 1024;
+constexpr int kNormPiece = 32768;    // elements a workgroup sums at a time
+constexpr uint32_t kNormGrid = 256;  // workgroups, and partial sums, per launch
 struct GradNormArgs {
   const void* g[kNormList];
   int64_t n[kNormList];
   uint32_t first[kNormList];  // first piece of each tensor
   int count;
   uint32_t pieces;
+  uint32_t sums, at;          // partial sums of the whole call, and the first of this launch
   double* partials;
+  uint64_t* arrived;          // workgroups of the call that have stored theirs; 0 between calls
+  double max_norm, inv_scale;
+  float* control;
 };
 static_assert(sizeof(GradNormArgs) <= 4096, "kernel arguments");
-hipError_t launch_grad_squares(const GradNormArgs& a, int g_dtype, uint32_t grid, hipStream_t st);
-hipError_t launch_grad_norm(const double* partials, int count, double max_norm, double inv_scale, float* control,
-                            hipStream_t st);
+hipError_t launch_grad_norm(const GradNormArgs& a, int g_dtype, uint32_t grid, hipStream_t st);
 
 // Group norm with activation (deft_norm_fwd.hip, deft_norm_bwd.hip).  A group
 // of an image, or a band of whole groups where channels come last, is cut into
@@ -191,7 +193,7 @@ struct NormArgs {
   float* sums;        // backward, several slices: [n][g][2] sums of gamma dz and of gamma dz h
   void* dgamma;       // backward, nullable; written by the main kernel where `arrivals` is set
   void* dbeta;
-  uint64_t* arrivals; // [bands or groups]: workgroups that have written their sums, over all calls
+  uint64_t* arrivals; // [bands or groups]: workgroups that have written their sums, 0 between calls
   int n, c, s, g, per, act;
   float eps;
   int slices, rp;     // channels last: rows (positions) per slice; first: channels per slice

@@ -98,8 +98,24 @@ __device__ __forceinline__ int anew(int v) {
 // rounds into each other until registers spill.
 __device__ __forceinline__ void apart() { __builtin_amdgcn_sched_barrier(0); }
 
-// exp(x) as 2^(x log2 e); the product's rounding costs x 2^-24 of the result.
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+// exp(x) as 2^(x log2 e), and 1 / x.  For bf16 results the hardware's
+// approximations are enough: the product's rounding costs x 2^-24 of the result.
+// fp32 silu takes that rounding back, and one Newton step (the error of its sums
+// falls from 2.2e-7 to 1e-7 for two operations in ten more).
+template <typename T> __device__ __forceinline__ float exp_of(float x) {
+  const float t = x * 1.44269504f, e = __builtin_amdgcn_exp2f(t);
+  if (sizeof(T) == 2) return e;
+  // what t lacks: its rounding, and log2 e beyond fp32
+  const float r = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269504f, -t));
+  const float more = e * (r * 0.693147181f);
+  return e + (__builtin_fabsf(t) < 127.f ? more : 0.f);  // zeros, infinities and NaN stay
+}
+template <typename T> __device__ __forceinline__ float inverse_of(float x) {
+  const float r = __builtin_amdgcn_rcpf(x);
+  if (sizeof(T) == 2) return r;
+  const float s = __builtin_fmaf(__builtin_fmaf(-x, r, 1.f), r, r);
+  return x < 1e38f ? s : r;  // where x r is no longer near 1
+}
 
 // Upper tail Q(a) = P(N > a) of the normal distribution, a >= 0, given e =
 // exp(-a^2/2): e t P(t) with t = 1 / (1 + p a), the form of Hastings' (1955)
@@ -134,9 +150,9 @@ template <typename T> __device__ __forceinline__ float normal_tail(float a, floa
 // A NaN stays a NaN in every activation.
 template <typename T, int ACT> __device__ __forceinline__ float act_of(float z) {
   if (ACT == DEFT_ACT_RELU) return z < 0.f ? 0.f : z;
-  if (ACT == DEFT_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + exp_of(-z));
+  if (ACT == DEFT_ACT_SILU) return z * inverse_of<T>(1.f + exp_of<T>(-z));
   if (ACT == DEFT_ACT_GELU) {
-    const float q = normal_tail<T>(__builtin_fabsf(z), exp_of(-0.5f * z * z));
+    const float q = normal_tail<T>(__builtin_fabsf(z), exp_of<bf16_t>(-0.5f * z * z));
     return z * (z > 0.f ? 1.f - q : q);
   }
   return z;
@@ -145,11 +161,11 @@ template <typename T, int ACT> __device__ __forceinline__ float act_of(float z) 
 template <typename T, int ACT> __device__ __forceinline__ float act_grad(float z, float dy) {
   if (ACT == DEFT_ACT_RELU) return z > 0.f ? dy : 0.f;
   if (ACT == DEFT_ACT_SILU) {
-    const float p = __builtin_amdgcn_rcpf(1.f + exp_of(-z));
+    const float p = inverse_of<T>(1.f + exp_of<T>(-z));
     return dy * (p * __builtin_fmaf(z, 1.f - p, 1.f));
   }
   if (ACT == DEFT_ACT_GELU) {
-    const float e = exp_of(-0.5f * z * z);
+    const float e = exp_of<bf16_t>(-0.5f * z * z);
     const float q = normal_tail<T>(__builtin_fabsf(z), e);
     return dy * __builtin_fmaf(z * 0.3989422804f, e, z > 0.f ? 1.f - q : q);
   }

@@ -69,22 +69,26 @@ __device__ __forceinline__ void put_part(float* p, float v) {
 // that have them (one slice each): small calls, which take longer to launch than
 // to run, save a launch by it.
 // Each wave waits for its stores of A and B (stored), then, past a barrier, one
-// thread counts the workgroup in (arrive; arrivals are counted on from call to
-// call) while dx is computed, and at the end the last one adds up.
+// thread counts the workgroup in (arrive) while dx is computed, and at the end
+// the last one adds up.
 __device__ __forceinline__ void stored() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint64_t arrive(const NormArgs& a, int unit) {
   if (!a.arrivals || threadIdx.x) return 0;
   return __hip_atomic_fetch_add(a.arrivals + unit, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 template <typename T>
-__device__ __forceinline__ void params_by_last(const NormArgs& a, uint64_t ticket, int c0, int cols, float* lds) {
+__device__ __forceinline__ void params_by_last(const NormArgs& a, uint64_t ticket, int unit, int c0, int cols, float* lds) {
   if (!a.arrivals) return;
   __shared__ int last;
-  if (threadIdx.x == 0) last = (ticket + 1) % (uint32_t)a.n == 0;
+  if (threadIdx.x == 0) {
+    last = ticket + 1 == (uint64_t)a.n;
+    if (last)  // for the next call
+      __hip_atomic_store(a.arrivals + unit, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
   __syncthreads();
   if (!last) return;
   const int nt = blockDim.x, rows = a.n, wide = min(cols, nt);
-  const int shares = nt / wide, share = threadIdx.x / wide, lane = threadIdx.x - share * wide;
+  const int shares = min(nt / wide, 16), share = threadIdx.x / wide, lane = threadIdx.x - share * wide;
   for (int col = lane; col - lane < cols; col += wide) {
     float va = 0.f, vb = 0.f;
     if (share < shares && col < cols) {
@@ -336,7 +340,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd_last(const NormArgs a
       load_rows(r0);
     }
   });
-  if (MODE == kNormWhole) params_by_last<T>(a, ticket, w.c0, w.cols, lds);
+  if (MODE == kNormWhole) params_by_last<T>(a, ticket, b, w.c0, w.cols, lds);
 }
 
 // Channels first; blocks as in the forward.  part: [n][ws][2][c], A and B of
@@ -533,7 +537,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd_first(const NormArgs 
       if (i - first >= ic * t) { i = first; row += teams; }
     }
   });
-  if (MODE == kNormWhole) params_by_last<T>(a, ticket, g * a.per, a.per, lds);
+  if (MODE == kNormWhole) params_by_last<T>(a, ticket, g, g * a.per, a.per, lds);
 }
 
 // S1 and S2 of each group of each image from the slices' A and B.  A thread has

@@ -69,7 +69,7 @@ bool whole_pays(const deft_norm_desc& d, bool back, int V, int rounds, int64_t u
   if (rounds > (V == 1 || back ? 16 : 32)) return false;
   if (units >= kCus * 3 / 4) return true;
   const int ops = (d.act == DEFT_ACT_GELU ? 40 : d.act == DEFT_ACT_SILU ? 24 : 12) * (back ? 2 : 1);
-  return elems * ops <= (back ? 600000 : 400000);
+  return elems * ops <= (back ? 1000000 : 400000);
 }
 
 // Channels last.  Whole: bands of groups, 32 bytes of each row or more (64
@@ -292,17 +292,17 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
     y.m_scale = x.m_scale; y.v_scale = x.v_scale;
     y.master = x.master;
     y.n = x.n;
-    y.wd = x.weight_decay;
-    y.decay = (float)(1.0 - d->lr * x.weight_decay);
-    y.id = (uint32_t)i;
+    y.decay = schedule ? x.weight_decay : 1.0 - d->lr * x.weight_decay;
+    a.id[a.count] = (uint32_t)i;
     a.first[a.count++] = (uint32_t)blocks;
     blocks += more;
   }
   return DEFT_OK;
 }
 
+// The workgroups' counter, then their sums.
 size_t deft_grad_norm_workspace_bytes(int count) {
-  return (size_t)norm_launches(std::max(count, 0)) * deft::kNormGrid * sizeof(double);
+  return kAlign + (size_t)norm_launches(std::max(count, 0)) * deft::kNormGrid * sizeof(double);
 }
 
 int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtype, double max_norm,
@@ -324,29 +324,40 @@ int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtyp
   if (!aligned16(workspace)) return DEFT_ERR_ALIGN;
   deft::GradNormArgs a;
   std::memset(&a, 0, sizeof(a));
-  double* partials = (double*)workspace;
-  int sums = 0;
-  uint64_t pieces = 0;
-  for (int i = 0; i <= count; ++i) {
-    const uint64_t more = i < count ? blocks_of(n[i], deft::kNormPiece) : 0;
-    if (a.count && (i == count || (more && a.count == deft::kNormList))) {
-      a.pieces = (uint32_t)pieces;
-      a.partials = partials + sums;
-      const uint32_t grid = (uint32_t)std::min<uint64_t>(pieces, deft::kNormGrid);
-      const hipError_t e = deft::launch_grad_squares(a, g_dtype, grid, (hipStream_t)stream);
-      if (e != hipSuccess) return status_of(e);
-      sums += (int)grid;
-      a.count = 0;
-      pieces = 0;
+  a.arrived = (uint64_t*)workspace;
+  a.partials = (double*)((char*)workspace + kAlign);
+  a.max_norm = max_norm;
+  a.inv_scale = inv_scale;
+  a.control = control;
+  // first how many workgroups the launches have in all, then the launches; a list
+  // of no elements has one workgroup
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t sums = 0;
+    uint64_t pieces = 0;
+    a.count = 0;
+    for (int i = 0; i <= count; ++i) {
+      const uint64_t more = i < count ? blocks_of(n[i], deft::kNormPiece) : 0;
+      if ((a.count && (i == count || (more && a.count == deft::kNormList))) || (i == count && !sums)) {
+        const uint32_t grid = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(pieces, 1), deft::kNormGrid);
+        a.pieces = (uint32_t)pieces;
+        a.at = sums;
+        if (pass == 1) {
+          const hipError_t e = deft::launch_grad_norm(a, g_dtype, grid, (hipStream_t)stream);
+          if (e != hipSuccess) return status_of(e);
+        }
+        sums += grid;
+        a.count = 0;
+        pieces = 0;
+      }
+      if (!more) continue;
+      a.g[a.count] = g[i];
+      a.n[a.count] = n[i];
+      a.first[a.count++] = (uint32_t)pieces;
+      pieces += more;
     }
-    if (!more) continue;
-    a.g[a.count] = g[i];
-    a.n[a.count] = n[i];
-    a.first[a.count++] = (uint32_t)pieces;
-    pieces += more;
+    a.sums = sums;
   }
-  return status_of(
-      deft::launch_grad_norm(partials, sums, max_norm, inv_scale, control, (hipStream_t)stream));
+  return DEFT_OK;
 }
 
 int deft_norm_desc_validate(const deft_norm_desc* d) {

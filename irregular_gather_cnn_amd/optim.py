@@ -75,7 +75,7 @@ class GradNorm:
         count = len(grads.sizes)
         self._n = (ctypes.c_int64 * count)(*grads.sizes)
         self.ws_bytes = _lib.deft_grad_norm_workspace_bytes(count)
-        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=grads.device)
+        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=grads.device)
         self.control = torch.zeros(4, dtype=torch.float32, device=grads.device)
 
     def bind(self, grads):
