@@ -411,8 +411,8 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
  * (infinity: no clipping).  Writes control (device, 4 floats): {norm, factor,
  * 1 if every gradient is finite else 0, 0}; the factor is 0 where they are
  * not.  No gradient is changed: deft_adamw_step applies the factor.
- * DEFT_ERR_DTYPE, DEFT_ERR_BAD_DESC, DEFT_ERR_UNSUPPORTED, DEFT_ERR_NULLPTR,
- * DEFT_ERR_ALIGN (gradients, control and workspace 16 bytes),
+ * DEFT_ERR_DTYPE, DEFT_ERR_BAD_DESC, DEFT_ERR_UNSUPPORTED (over 2^44 elements),
+ * DEFT_ERR_NULLPTR, DEFT_ERR_ALIGN (gradients, control and workspace 16 bytes),
  * DEFT_ERR_WORKSPACE; checks run before any launch. */
 int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtype, double max_norm,
                    double inv_scale, float* control, void* workspace, size_t ws_bytes, void* stream);

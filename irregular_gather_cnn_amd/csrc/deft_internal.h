@@ -154,7 +154,7 @@ struct AdamwArgs {
 };
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
 hipError_t launch_adamw(const AdamwArgs& a, uint32_t blocks, int p_dtype, int g_dtype, int bits, bool master,
-                        hipStream_t st);
+                        bool once, hipStream_t st);
 constexpr int kSquareThreads = 1024;
 constexpr int kNormPiece = 32768;    // elements a workgroup sums at a time
 constexpr uint32_t kNormGrid = 256;  // workgroups, and partial sums, per launch

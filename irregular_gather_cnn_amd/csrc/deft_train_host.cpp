@@ -22,6 +22,11 @@ int status_of(hipError_t e) { return e == hipSuccess ? DEFT_OK : deft::report_hi
 // Workgroups of one launch stay below 2^31.
 constexpr uint64_t kMaxBlocks = 0x7fffffffu;
 
+// Gradients of one norm; their pieces stay below 2^31, too.
+constexpr uint64_t kMaxElems = 1ull << 44;
+constexpr double kCacheBytes = 256e6;
+
+int elem_size(int dtype) { return dtype == DEFT_BF16 ? 2 : 4; }
 uint64_t blocks_of(int64_t n, int64_t per) { return ((uint64_t)n + per - 1) / per; }
 
 int norm_launches(int count) { return std::max(1, (count + deft::kNormList - 1) / deft::kNormList); }
@@ -34,7 +39,6 @@ constexpr size_t kAlign = 256;
 
 size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-int elem_size(int dtype) { return dtype == DEFT_BF16 ? 2 : 4; }
 
 int norm_desc_status(const deft_norm_desc* d) {
   if (!d) return DEFT_ERR_NULLPTR;
@@ -274,13 +278,19 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
   a.seed = d->seed;
   a.control = control;
   a.schedule = schedule;
+  // A step over more than the last-level cache holds leaves nothing of itself there
+  // for the next one.
+  double elems = 0.0;
+  for (int i = 0; i < count; ++i) elems += (double)t[i].n;
+  const int weights = d->master ? 8 + elem_size(d->p_dtype) : 2 * elem_size(d->p_dtype);
+  const bool once = elems * (elem_size(d->g_dtype) + weights + (d->state_bits == 8 ? 4 : 16)) > kCacheBytes;
   uint64_t blocks = 0;
   for (int i = 0; i <= count; ++i) {
     const uint64_t more = i < count ? blocks_of(t[i].n, deft::kAdamwElems) : 0;
     // the list is full, or at its end: launch what it holds
     if (a.count && (i == count || (more && (a.count == deft::kAdamwList || blocks + more > kMaxBlocks)))) {
       const hipError_t e = deft::launch_adamw(a, (uint32_t)blocks, d->p_dtype, d->g_dtype, d->state_bits,
-                                              d->master != 0, (hipStream_t)stream);
+                                              d->master != 0, once, (hipStream_t)stream);
       if (e != hipSuccess) return status_of(e);
       a.count = 0;
       blocks = 0;
@@ -300,10 +310,9 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
   return DEFT_OK;
 }
 
-// The workgroups' counter, then their sums.
-size_t deft_grad_norm_workspace_bytes(int count) {
-  return kAlign + (size_t)norm_launches(std::max(count, 0)) * deft::kNormGrid * sizeof(double);
-}
+// The workgroups' counter, then their sums: 8 KB for each launch hold both.
+static_assert(kAlign + deft::kNormGrid * sizeof(double) <= 8192, "grad norm workspace");
+size_t deft_grad_norm_workspace_bytes(int count) { return (size_t)norm_launches(std::max(count, 0)) * 8192; }
 
 int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtype, double max_norm,
                    double inv_scale, float* control, void* workspace, size_t ws_bytes, void* stream) {
@@ -314,8 +323,8 @@ int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtyp
   for (int i = 0; i < count; ++i) {
     if (n[i] < 0) return DEFT_ERR_BAD_DESC;
     if (n[i] == 0) continue;
-    all += blocks_of(n[i], deft::kNormPiece);
-    if (all > kMaxBlocks) return DEFT_ERR_UNSUPPORTED;
+    all += (uint64_t)n[i];
+    if ((uint64_t)n[i] > kMaxElems || all > kMaxElems) return DEFT_ERR_UNSUPPORTED;
     if (!g[i]) return DEFT_ERR_NULLPTR;
     if (!aligned16(g[i])) return DEFT_ERR_ALIGN;
   }

@@ -448,3 +448,27 @@ def test_runs_on_the_current_stream_and_on_rebound_gradients():
         opt.step(control=opt.grad_norm(max_norm=math.inf, inv_scale=0.5))
     torch.cuda.current_stream().wait_stream(side)
     mir.check([other], "f32", coef=np.float32(0.5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits,master", [(8, True), (32, False)])
+def test_a_step_larger_than_the_caches_gives_the_same_bits(bits, master):
+    """Such a step accesses memory in another way; its first tensor's bits are those of a small step."""
+    big = 20_000_003
+    kind = "bf16" if master else "f32"
+    gen = torch.Generator().manual_seed(15)
+    p0, g0 = torch.randn(70_001, generator=gen) * 0.05, torch.randn(70_001, generator=gen) * 1e-3
+
+    def run(sizes):
+        p = [torch.zeros(n, dtype=TYPES[kind], device="cuda") for n in sizes]
+        g = [torch.full((n,), 1e-3, dtype=TYPES[kind], device="cuda") for n in sizes]
+        p[0].copy_(p0)
+        g[0].copy_(g0)
+        masters = [x.float() for x in p] if master else None
+        opt = AdamW(p, g, bits=bits, masters=masters, weight_decay=0.1, seed=3, **HYPER)
+        for _ in range(2):
+            opt.step()
+        return [opt.params[0]] + [t for t in opt.states[0] if t is not None] + ([masters[0]] if master else [])
+
+    for a, b in zip(run([70_001]), run([70_001, big])):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
