@@ -179,7 +179,11 @@ hipError_t launch_grad_norm(const GradNormArgs& a, int g_dtype, uint32_t grid, h
 // that the chip holds at once: statistics and result in one launch, in which
 // the slices' workgroups join their sums.  More: partial statistics, their
 // combination, and the result from a second read.
-constexpr int kNormThreads = 512;
+constexpr int kNormThreads = 512;   // 1024 where a kernel's registers allow it (kNormWide)
+constexpr int kNormWide = 1024;
+// Backward kernels that hold a group whole in 8 accesses a thread and 128 registers:
+// they run with 1024 threads what would take 16 accesses and half as many waves.
+constexpr bool norm_bwd_wide(bool fp32, bool last, bool keep) { return fp32 || !(last || keep); }
 enum NormMode { kNormWhole = 0, kNormJoint = 1, kNormStats = 2, kNormApply = 3 };
 struct NormArgs {
   const void* x;

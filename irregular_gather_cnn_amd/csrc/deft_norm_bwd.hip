@@ -14,6 +14,10 @@ namespace deft {
 
 namespace {
 
+template <typename T, int U, int MODE, bool KEEP> constexpr int bound(bool last) {
+  return MODE == kNormWhole && U == 8 && norm_bwd_wide(sizeof(T) == 4, last, KEEP) ? kNormWide : kNormThreads;
+}
+
 // Sums of the words of group g of a cluster, in every lane of a wave; false if
 // they did not come.
 __device__ __forceinline__ bool sum_joint(const NormArgs& a, const Joint& jt, int ng, int g, float& s1, float& s2) {
@@ -117,7 +121,7 @@ __device__ __forceinline__ void params_by_last(const NormArgs& a, uint64_t ticke
 // Channels last; blocks as in the forward.  part: [n][slices][2][c], A and B of
 // each slice.  Joint words: a slice's shares of S1 and S2.
 template <typename T, int V, int U, int MODE, bool KEEP>
-__global__ __launch_bounds__(kNormThreads) void k_norm_bwd_last(const NormArgs a) {
+__global__ __launch_bounds__((bound<T, U, MODE, KEEP>(true))) void k_norm_bwd_last(const NormArgs a) {
   extern __shared__ float lds[];
   int b, k, n;
   if (MODE == kNormJoint) {
@@ -346,13 +350,13 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd_last(const NormArgs a
 // Channels first; blocks as in the forward.  part: [n][ws][2][c], A and B of
 // each slice of the positions.  Joint words: a slice's shares of S1 and S2.
 template <typename T, int V, int U, int MODE, bool KEEP>
-__global__ __launch_bounds__(kNormThreads) void k_norm_bwd_first(const NormArgs a) {
+__global__ __launch_bounds__((bound<T, U, MODE, KEEP>(false))) void k_norm_bwd_first(const NormArgs a) {
   extern __shared__ float lds[];
   const int id = MODE == kNormJoint ? blockIdx.x : xcd_swizzle(blockIdx.x, gridDim.x);
   const int ng = id / a.slices, k = id - ng * a.slices, n = ng / a.g, g = ng - n * a.g;
   const int t = 1 << a.lt, ln = threadIdx.x & (t - 1), tm = threadIdx.x >> a.lt, teams = blockDim.x >> a.lt;
   const int subs = t > 64 ? t >> 6 : 1;  // waves that share a channel
-  float* gam = lds + 16;
+  float* gam = lds + 32;
   float* bet = gam + a.rp;
   float* ra = bet + a.rp;                // [rows][subs]
   float* rb = ra + a.rp * subs;
@@ -462,7 +466,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd_first(const NormArgs 
     if (MODE == kNormStats) return;
     s1 = block_sum(s1, lds);
     if (MODE == kNormWhole && a.arrivals) stored();
-    s2 = block_sum(s2, lds + 8);
+    s2 = block_sum(s2, lds + 16);
   };
   float s1, s2;
   if (MODE == kNormWhole) {

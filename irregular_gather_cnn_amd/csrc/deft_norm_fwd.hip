@@ -21,21 +21,18 @@ __device__ __forceinline__ float slice_count(const NormArgs& a, int layout, int 
   return (float)min(a.rp, a.per - kr * a.rp) * (float)min(a.cp, a.s - ks * a.cp);
 }
 
-// A group's mean and rstd from its slices' mean and M2, a wave's work: sums
-// over the lanes' slices in fp64, which squares of means far from zero need.
+// A group's mean and rstd from its slices' mean and M2: sums over the lanes'
+// slices in fp64, which squares of means far from zero need.
 struct Combine {
   double sum = 0.0, squares = 0.0;
   __device__ __forceinline__ void add(float count, float mean, float m2) {
     sum += (double)count * mean;
     squares += (double)m2 + (double)count * mean * mean;
   }
-  __device__ __forceinline__ void finish(const NormArgs& a, float& mean, float& rstd) {
-    for (int d = 32; d > 0; d >>= 1) {
-      sum += __shfl_xor(sum, d);
-      squares += __shfl_xor(squares, d);
-    }
-    const double count = (double)a.s * a.per, m = sum / count;
-    double var = squares / count - m * m;
+  // of the sums over all lanes
+  __device__ __forceinline__ void finish(const NormArgs& a, float& mean, float& rstd) const {
+    const double inv = 1.0 / ((double)a.s * a.per), m = sum * inv;
+    double var = squares * inv - m * m;
     var = var < 0.0 ? 0.0 : var;  // a NaN stays
     mean = (float)m;
     rstd = 1.f / __builtin_sqrtf((float)var + a.eps);
@@ -47,6 +44,8 @@ __device__ __forceinline__ bool combine_joint(const NormArgs& a, int layout, con
   Combine c;
   if (!jt.gather(a.slices, ng, g, [&](int k, float m, float m2) { c.add(slice_count(a, layout, k), m, m2); }))
     return false;
+  c.sum = team_sum(c.sum, 64);
+  c.squares = team_sum(c.squares, 64);
   c.finish(a, mean, rstd);
   return true;
 }
@@ -563,12 +562,15 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
   });
 }
 
-// mean and rstd of each group of each image from its slices: a wave per group.
-__global__ __launch_bounds__(64) void k_norm_combine(const NormArgs a, int layout) {
+// mean and rstd of each group of each image from its slices.
+__global__ __launch_bounds__(256) void k_norm_combine(const NormArgs a, int layout) {
+  __shared__ double lds[8];
   const int ng = blockIdx.x;
   const float2* p = (const float2*)a.part + (size_t)ng * a.slices;
   Combine c;
-  for (int k = threadIdx.x; k < a.slices; k += 64) c.add(slice_count(a, layout, k), p[k].x, p[k].y);
+#pragma unroll 4
+  for (int k = threadIdx.x; k < a.slices; k += 256) c.add(slice_count(a, layout, k), p[k].x, p[k].y);
+  block_sums(c.sum, c.squares, lds);
   float mean, rstd;
   c.finish(a, mean, rstd);
   if (threadIdx.x == 0) {
@@ -616,7 +618,7 @@ hipError_t launch_norm_fwd(const NormArgs& a, const NormPlan& p, int layout, int
 }
 
 hipError_t launch_norm_combine(const NormArgs& a, int layout, hipStream_t st) {
-  DEFT_LAUNCH("norm_combine", k_norm_combine, dim3((unsigned)(a.n * a.g)), dim3(64), 0, st, a, layout);
+  DEFT_LAUNCH("norm_combine", k_norm_combine, dim3((unsigned)(a.n * a.g)), dim3(256), 0, st, a, layout);
   return hipGetLastError();
 }
 

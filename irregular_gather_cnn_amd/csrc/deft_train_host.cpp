@@ -76,6 +76,13 @@ bool whole_pays(const deft_norm_desc& d, bool back, int V, int rounds, int64_t u
   return elems * ops <= (back ? 1000000 : 400000);
 }
 
+// 9 to 16 accesses of 512 threads as up to 8 of 1024.
+bool goes_wide(const deft_norm_desc& d, bool back, int V, int rounds) {
+  const bool keep = d.dtype == DEFT_BF16 && d.act >= DEFT_ACT_SILU;
+  return back && V > 1 && rounds > 8 && rounds <= 16 &&
+         deft::norm_bwd_wide(d.dtype == DEFT_F32, d.layout == DEFT_CHANNELS_LAST, keep);
+}
+
 // Channels last.  Whole: bands of groups, 32 bytes of each row or more (64
 // backward from 2^20 elements on, where the lines that bands share no longer
 // come from the cache: 16x784x512 bf16 takes 20 us against 24).  Else slices of
@@ -93,6 +100,10 @@ void cut_last(const deft_norm_desc& d, bool back, NormCut& r) {
   int bands = std::max(1, g / std::min(g, ceil_div(wide, per * esz)));
   while (bands > 1 && g / bands * per < V) --bands;
   int rounds = ceil_div(d.s, nt / widest(bands));
+  if (goes_wide(d, back, V, rounds)) {
+    nt = deft::kNormWide;
+    rounds = 8;  // the kernel for it; half as many as before are needed
+  }
   r.mode = deft::kNormWhole;
   r.a.slices = 1;
   r.a.rp = d.s;
@@ -157,6 +168,12 @@ void cut_first(const deft_norm_desc& d, bool back, NormCut& r) {
   int nt = 64;
   int rounds = best_team(nt, per, chunks, &r.a.lt);
   while (rounds > 4 && nt < deft::kNormThreads) rounds = best_team(nt *= 2, per, chunks, &r.a.lt);
+  int lt = 0;
+  if (goes_wide(d, back, V, rounds) && best_team(deft::kNormWide, per, chunks, &lt) <= 8) {
+    nt = deft::kNormWide;
+    rounds = 8;  // the kernel for it
+    r.a.lt = lt;
+  }
   r.mode = deft::kNormWhole;
   r.a.rp = per;
   r.a.ws = 1;
@@ -181,7 +198,7 @@ void cut_first(const deft_norm_desc& d, bool back, NormCut& r) {
   r.p.threads = nt;
   r.p.u = rounds;
   const int subs = std::max(1, (1 << r.a.lt) >> 6);
-  r.p.lds = sizeof(float) * (back ? std::max(2 * nt, 16 + (2 + 2 * subs) * r.a.rp) : 32 + 2 * r.a.rp);
+  r.p.lds = sizeof(float) * (back ? std::max(2 * nt, 32 + (2 + 2 * subs) * r.a.rp) : 32 + 2 * r.a.rp);
 }
 
 int norm_cut(const deft_norm_desc& d, bool back, NormCut& r) {
