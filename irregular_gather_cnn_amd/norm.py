@@ -6,6 +6,8 @@ in ``_lib``.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -42,33 +44,43 @@ class GroupNormAct:
         self.device = self.ws.device
         self._index = self.ws.get_device()
         self._stats = torch.empty((n, groups), dtype=torch.float32, device=device)
-        image, channel, stat = (n * c * s, self.tdtype), (c, self.tdtype), (n * groups, torch.float32)
-        self._kinds = dict(x=image, y=image, dy=image, dx=image, gamma=channel, beta=channel, dgamma=channel,
-                           dbeta=channel, mean=stat, rstd=stat)
+        # what each argument must be: elements and dtype
+        self._image, self._channel, self._stat = (n * c * s, self.tdtype), (c, self.tdtype), (n * groups, torch.float32)
+        self._kinds = dict(mean=self._stat, rstd=self._stat)
+        self._kinds.update({k: self._image for k in ("x", "y", "dy", "dx")})
+        self._kinds.update({k: self._channel for k in ("gamma", "beta", "dgamma", "dbeta")})
 
-    def _check(self, **tensors):
+        # small calls wait for the host: the C functions are called without the binding's wrappers
+        lib, self._ref, self._ws = _lib.load(), ctypes.byref(self.desc), self.ws.data_ptr()
+        self._forward, self._backward = lib.deft_norm_forward, lib.deft_norm_backward
+
+    def _unfit(self, t, kind):
+        return (t.numel() != kind[0] or t.dtype is not kind[1] or t.get_device() != self._index
+                or not t.is_contiguous())
+
+    def _refuse(self, **tensors):
         for what, t in tensors.items():
-            size, dtype = self._kinds[what]
-            if t.numel() != size or t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous():
-                raise ValueError("%s must be %d contiguous elements of %s on %s" % (what, size, dtype, self.device))
+            if t is not None and self._unfit(t, self._kinds[what]):
+                raise ValueError("%s must be %d contiguous elements of %s on %s" % (
+                    (what,) + self._kinds[what] + (self.device,)))
 
     def forward(self, x, gamma, beta, y=None, mean=None, rstd=None):
         """(y, mean, rstd); mean and rstd are float32 [n][groups]."""
-        self._check(x=x, gamma=gamma, beta=beta)
+        unfit = self._unfit
+        if unfit(x, self._image) or unfit(gamma, self._channel) or unfit(beta, self._channel):
+            self._refuse(x=x, gamma=gamma, beta=beta)
+        if y is not None or mean is not None or rstd is not None:
+            self._refuse(y=y, mean=mean, rstd=rstd)
         if y is None:
             y = torch.empty_like(x)
-        else:
-            self._check(y=y)
         if mean is None:
             mean = torch.empty_like(self._stats)
-        else:
-            self._check(mean=mean)
         if rstd is None:
             rstd = torch.empty_like(self._stats)
-        else:
-            self._check(rstd=rstd)
-        _lib.deft_norm_forward(self.desc, x, gamma, beta, y, mean, rstd, self.ws, self.ws_bytes,
-                               current_stream(self.device))
+        code = self._forward(self._ref, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(), mean.data_ptr(),
+                             rstd.data_ptr(), self._ws, self.ws_bytes, current_stream(self.device))
+        if code:
+            raise _lib.DeftError(code, "deft_norm_forward")
         return y, mean, rstd
 
     def backward(self, x, gamma, beta, mean, rstd, dy, out=None):
@@ -76,13 +88,20 @@ class GroupNormAct:
         holds as None is not computed."""
         if not self.training:
             raise ValueError("backward needs training=True")
-        self._check(x=x, gamma=gamma, beta=beta, mean=mean, rstd=rstd, dy=dy)
+        unfit = self._unfit
+        if (unfit(x, self._image) or unfit(gamma, self._channel) or unfit(beta, self._channel)
+                or unfit(dy, self._image) or unfit(mean, self._stat) or unfit(rstd, self._stat)):
+            self._refuse(x=x, gamma=gamma, beta=beta, mean=mean, rstd=rstd, dy=dy)
         if out is None:
             out = dict(dx=torch.empty_like(x), dgamma=torch.empty_like(gamma), dbeta=torch.empty_like(beta))
         else:
-            self._check(**{k: t for k, t in out.items() if t is not None})
-        _lib.deft_norm_backward(self.desc, x, gamma, beta, mean, rstd, dy, out["dx"], out["dgamma"], out["dbeta"],
-                                self.ws, self.ws_bytes, current_stream(self.device))
+            self._refuse(dx=out["dx"], dgamma=out["dgamma"], dbeta=out["dbeta"])
+        dx, dgamma, dbeta = (None if out[k] is None else out[k].data_ptr() for k in ("dx", "dgamma", "dbeta"))
+        code = self._backward(self._ref, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), mean.data_ptr(),
+                              rstd.data_ptr(), dy.data_ptr(), dx, dgamma, dbeta, self._ws, self.ws_bytes,
+                              current_stream(self.device))
+        if code:
+            raise _lib.DeftError(code, "deft_norm_backward")
         return out
 
 

@@ -77,14 +77,18 @@ class GradNorm:
         self.ws_bytes = _lib.deft_grad_norm_workspace_bytes(count)
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=grads.device)
         self.control = torch.zeros(4, dtype=torch.float32, device=grads.device)
+        # small lists wait for the host: the C function is called without the binding's wrapper
+        self._call, self._ws, self._out = _lib.load().deft_grad_norm, self.ws.data_ptr(), self.control.data_ptr()
 
     def bind(self, grads):
         self.grads.bind(grads)
 
     def __call__(self, max_norm=float("inf"), inv_scale=1.0):
         g = self.grads
-        _lib.deft_grad_norm(g.pointers, self._n, len(g.sizes), g.dtype, max_norm, inv_scale, self.control, self.ws,
-                            self.ws_bytes, current_stream(g.device))
+        code = self._call(g.pointers, self._n, len(g.sizes), g.dtype, max_norm, inv_scale, self._out, self._ws,
+                          self.ws_bytes, current_stream(g.device))
+        if code:
+            raise _lib.DeftError(code, "deft_grad_norm")
         return self.control
 
 
@@ -137,6 +141,7 @@ class AdamW:
                 p.data_ptr(), self.grads.pointers[k], m.data_ptr(), v.data_ptr(), ms.data_ptr() if bits == 8 else None,
                 vs.data_ptr() if bits == 8 else None, self.masters[k].data_ptr() if self.masters else None,
                 self.sizes[k], decay[k])
+        self._call, self._ref = _lib.load().deft_adamw_step, ctypes.byref(self._desc)
         self._norm = GradNorm.__new__(GradNorm)
         self._norm._setup(self.grads)
 
@@ -182,11 +187,15 @@ class AdamW:
         read in place of the host's, for a step captured in a graph."""
         if lr is not None:
             self.lr = lr
-        for what, t, n, kind in (("control", control, 4, torch.float32), ("schedule", schedule, 4, torch.float64)):
-            if t is not None and (t.numel() != n or t.dtype != kind or t.device != self.device
-                                  or not t.is_contiguous()):
-                raise ValueError("%s must be %d contiguous elements of %s on %s" % (what, n, kind, self.device))
+        if control is not None or schedule is not None:
+            for what, t, kind in (("control", control, torch.float32), ("schedule", schedule, torch.float64)):
+                if t is not None and (t.numel() != 4 or t.dtype != kind or t.device != self.device
+                                      or not t.is_contiguous()):
+                    raise ValueError("%s must be 4 contiguous elements of %s on %s" % (what, kind, self.device))
         d = self._desc
         d.lr, d.step, d.seed = self.lr, self.steps + 1, self.step_seed(self.steps + 1)
-        _lib.deft_adamw_step(d, self._list, len(self.params), control, schedule, current_stream(self.device))
+        code = self._call(self._ref, self._list, len(self.params), None if control is None else control.data_ptr(),
+                          None if schedule is None else schedule.data_ptr(), current_stream(self.device))
+        if code:
+            raise _lib.DeftError(code, "deft_adamw_step")
         self.steps += 1
