@@ -619,17 +619,13 @@ template <typename T, int V, int U>
 hipError_t launch_mode(const NormArgs& a, const NormPlan& p, int layout, int mode, hipStream_t st) {
   constexpr bool can = V == 8 && U <= 8;  // 16 chunks and their dz fill the registers
   const bool keep = can && (a.act == DEFT_ACT_SILU || a.act == DEFT_ACT_GELU);
-  switch (mode) {
-    case kNormWhole:
-      return keep ? launch<T, V, U, kNormWhole, can>(a, p, layout, st)
-                  : launch<T, V, U, kNormWhole, false>(a, p, layout, st);
-    case kNormJoint:
+  if (mode == kNormWhole)
+    return keep ? launch<T, V, U, kNormWhole, can>(a, p, layout, st)
+                : launch<T, V, U, kNormWhole, false>(a, p, layout, st);
+  if constexpr (U <= 8 || V == 1) {  // slices have no more
+    if (mode == kNormJoint)
       return keep ? launch<T, V, U, kNormJoint, can>(a, p, layout, st)
                   : launch<T, V, U, kNormJoint, false>(a, p, layout, st);
-    default:
-      break;
-  }
-  if constexpr (U <= 8 || V == 1) {  // slices that are read twice have no more
     return mode == kNormStats ? launch<T, V, U, kNormStats, false>(a, p, layout, st)
                               : launch<T, V, U, kNormApply, false>(a, p, layout, st);
   }

@@ -88,7 +88,10 @@ bool goes_wide(const deft_norm_desc& d, bool back, int V, int rounds) {
 // come from the cache: 16x784x512 bf16 takes 20 us against 24).  Else slices of
 // whole rows, of 1024 channels at most, of 4 to 8 accesses a thread (fewer when
 // they would leave compute units idle: 443 slices of 4 rows took 18 us where 111
-// of 16 take 14).
+// of 16 take 14).  Every slice has all groups here, so the exchange grows with
+// both, and from 2^21 elements on a second read costs less: forward 33.5 M elements
+// in bf16 with gelu 94 us joined and 56 read twice, 8.9 M 24 and 19, 1.4 M 11.3 and
+// 12.2; backward 24.4 M 93 and 78, 7.1 M in fp32 48 and 38, 1.3 M 18 and 19.
 void cut_last(const deft_norm_desc& d, bool back, NormCut& r) {
   const int per = r.a.per, g = d.groups, esz = elem_size(d.dtype);
   const int V = d.c >= 16 / esz ? 16 / esz : 1;
@@ -114,20 +117,17 @@ void cut_last(const deft_norm_desc& d, bool back, NormCut& r) {
     rounds = 8;
     auto slices = [&] { return ceil_div(d.s, (int64_t)ty * rounds); };
     while (rounds > 4 && (int64_t)d.n * bands * slices() < kCus) rounds /= 2;
-    if (back && slices() > resident(back, nt)) {  // the largest slices there are
-      nt = deft::kNormThreads;
-      ty = nt / widest(bands);
-      rounds = 16;
-    }
-    r.mode = slices() <= resident(back, nt) ? deft::kNormJoint : deft::kNormStats;
+    const bool joint = (int64_t)d.n * d.s * d.c < 1 << 21 && slices() <= resident(back, nt);
+    r.mode = joint ? deft::kNormJoint : deft::kNormStats;
     r.a.rp = ty * rounds;
     if (back && r.mode == deft::kNormStats) {
-      // read twice: small accumulating workgroups, four on each unit, whose slices'
-      // sums are few; no slice over 64 accesses, to keep the chains of sums short
+      // read twice: small accumulating workgroups, two on each unit (20.4 M elements in
+      // bf16 take 48 us; four or one a unit 52 and 64), whose slices' sums are few; no
+      // slice over 64 accesses, to keep the chains of sums short
       nt = widest(bands) <= 256 ? 256 : deft::kNormThreads;
       ty = nt / widest(bands);
       rounds = 4;
-      const int blocks = ceil_div(d.s, ty * rounds), want = std::max(1, 4 * kCus / std::max(1, d.n * bands));
+      const int blocks = ceil_div(d.s, ty * rounds), want = std::max(1, 2 * kCus / std::max(1, d.n * bands));
       r.a.rp = std::min(ceil_div(blocks, std::min(blocks, want)), 16) * ty * rounds;
     }
     r.a.slices = ceil_div(d.s, r.a.rp);

@@ -421,7 +421,7 @@ def no_patience():
 # groups that several workgroups hold: few and many slices, along rows, channels and positions, and
 # words that each workgroup reads or that are first summed up
 JOINT = [(2, 320, 4099, 32), (1, 64, 20001, 1), (1, 3, 50001, 1), (3, 96, 9000, 48), (1, 512, 3000, 2),
-         (2, 1920, 700, 480)]
+         (2, 1920, 700, 480), (1, 1920, 700, 480), (2, 320, 1501, 32), (1, 100, 9001, 50)]
 
 
 @pytest.mark.gpu
