@@ -53,6 +53,10 @@ __device__ __forceinline__ bool combine_joint(const NormArgs& a, int layout, con
 // Channels last: slice k of band b of image n.  Blocks are in the order ((n, k), b),
 // so that the workgroups of one XCD share the lines of neighbouring bands; joint
 // ones in the order ((n, b), k) over all XCDs, so that a cluster starts together.
+// Bound by memory from a few million elements on: 32x1024x512 fp32 takes 23 us (5.8
+// TB/s), 2x65536x320 bf16 53 (read twice: 4.7 TB/s the first time, then 5.7); by
+// vector operations with gelu in bf16 (27 an element; 16x784x512 15 us against 11);
+// by latency below: load, reduction and store take 5 us, an exchange 3 to 5 more.
 // part: [n][g][slices]{mean, M2}.
 template <typename T, int V, int U, int MODE>
 __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_norm_fwd_last(const NormArgs a) {
@@ -354,6 +358,8 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
 
 // Channels first: slice (kr, ks) of a group of an image: channels kr * rp ...,
 // positions ks * cp ....  Teams of 2^lt lanes walk a channel's positions.
+// Bound by memory: 16x256x56x56 bf16 takes 12 to 13 us in one slice a group (4.3
+// TB/s), 2x320x65536 bf16 41 joined (4.1 TB/s).
 // part: [n][g][slices]{mean, M2}.
 template <typename T, int V, int U, int MODE>
 __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_norm_fwd_first(const NormArgs a) {
