@@ -64,16 +64,19 @@ int resident(bool back, int threads) { return kCus * (back ? 512 : 1024) / threa
 
 // One slice for a group (or a band of groups), where it fits the registers:
 // 32 accesses a thread forward, 16 of x and of dy backward.  It needs no
-// exchange, which costs 4 to 5 us, but only as many compute units work as there
-// are groups; so where these leave units idle, it pays up to about 3 us of one
-// unit's vector operations.  Measured forward (gelu, fp32, us in one slice and
-// joined): 27 groups of 4000 elements 8.6 and 10.5; 2x14 groups of 12136 18.7
-// and 10.9; 25 groups of 31878 19.3 and 13.8.
+// exchange, which costs 3 to 5 us, but only as many compute units work as there
+// are groups; so where these leave units idle, it pays up to about 5 us of one
+// unit's work, counted in vector operations an element, of which reading and
+// writing it forward cost as much as 26 in bf16 and 52 in fp32.  Measured forward
+// (us in one slice and joined): 12 bands of 9000 elements, gelu fp32, 8.6 and 10.7;
+// 5 groups of 20252, relu bf16, 6.1 and 7.1; 10 of 43590, none bf16, 10.2 and 8.6; 50
+// of 42476, none fp32, 18.7 and 10.9.
 bool whole_pays(const deft_norm_desc& d, bool back, int V, int rounds, int64_t units, int64_t elems) {
   if (rounds > (V == 1 || back ? 16 : 32)) return false;
   if (units >= kCus * 3 / 4) return true;
-  const int ops = (d.act == DEFT_ACT_GELU ? 40 : d.act == DEFT_ACT_SILU ? 24 : 12) * (back ? 2 : 1);
-  return elems * ops <= (back ? 1000000 : 400000);
+  const int act = d.act == DEFT_ACT_GELU ? 40 : d.act == DEFT_ACT_SILU ? 24 : 12;
+  if (back) return elems * act * 2 <= 1000000;
+  return elems * std::max(act, d.dtype == DEFT_F32 ? 52 : 26) <= 800000;
 }
 
 // 9 to 16 accesses of 512 threads as up to 8 of 1024.
