@@ -97,10 +97,19 @@ __device__ __forceinline__ void params_by_last(const NormArgs& a, uint64_t ticke
     float va = 0.f, vb = 0.f;
     if (share < shares && col < cols) {
       const float* p = a.part + c0 + col;
-#pragma unroll 4
-      for (int r = share; r < rows; r += shares) {
-        va += __hip_atomic_load(p + (size_t)r * 2 * a.c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        vb += __hip_atomic_load(p + ((size_t)r * 2 + 1) * a.c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int r0 = share; r0 < rows; r0 += 16 * shares) {  // 16 at once: each load takes a microsecond
+        float xa[16], xb[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float* at = p + (size_t)min(r0 + i * shares, rows - 1) * 2 * a.c;
+          xa[i] = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          xb[i] = __hip_atomic_load(at + a.c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          va += r0 + i * shares < rows ? xa[i] : 0.f;
+          vb += r0 + i * shares < rows ? xb[i] : 0.f;
+        }
       }
       lds[threadIdx.x] = va;
       lds[nt + threadIdx.x] = vb;
