@@ -175,7 +175,7 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(true))) void k_norm_bwd_la
     }
   };
   auto load = [&](int slice) {
-    end = min((slice + 1) * a.rp, a.s);
+    end = (int)min((uint32_t)(slice + 1) * (uint32_t)a.rp, (uint32_t)a.s);  // the product may pass 2^31
     load_rows(slice * a.rp);
   };
   const Ahead<T> gamma((const T*)a.gamma + w.c0, w.cols), beta((const T*)a.beta + w.c0, w.cols);
@@ -236,8 +236,8 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(true))) void k_norm_bwd_la
           }
         }
       }
+      if (MODE != kNormStats || end - r0 <= w.TY * U) break;  // only slices that are read twice are longer
       r0 += w.TY * U;
-      if (MODE != kNormStats || r0 >= end) break;  // only slices that are read twice are longer
       load_rows(r0);
     }
     if (w.ty < w.TY) {
@@ -352,8 +352,8 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(true))) void k_norm_bwd_la
           p += step;
         }
       }
+      if (MODE != kNormApply || end - r0 <= w.TY * U) break;
       r0 += w.TY * U;
-      if (MODE != kNormApply || r0 >= end) break;
       load_rows(r0);
     }
   });
@@ -377,9 +377,9 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(false))) void k_norm_bwd_f
   float* rb = ra + a.rp * subs;
   int r0, c0, rows, cols, chunks, ic, rounds, ks;
   auto slot = [&](int row, int i, int& pos, int& shift) {
-    const int want = c0 + i * V;
-    pos = want + V <= a.s ? want : a.s - V;  // s >= V
-    shift = want - pos;
+    const uint32_t want = (uint32_t)c0 + (uint32_t)i * V;  // past a row of 2^31 - 1, too
+    pos = want + V <= (uint32_t)a.s ? (int)want : a.s - V;  // s >= V
+    shift = (int)(want - pos);
     return row < rows && i < chunks;
   };
   Chunk<T, V> q[U], h[U];

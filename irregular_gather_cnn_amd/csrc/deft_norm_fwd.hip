@@ -373,9 +373,9 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
   // round u: channel tm + teams * (u / ic), chunk ln + t * (u % ic); a ragged
   // row's last chunk starts early enough to end with the row
   auto slot = [&](int row, int i, int& pos, int& shift) {
-    const int want = c0 + i * V;
-    pos = want + V <= a.s ? want : a.s - V;  // s >= V
-    shift = want - pos;
+    const uint32_t want = (uint32_t)c0 + (uint32_t)i * V;  // past a row of 2^31 - 1, too
+    pos = want + V <= (uint32_t)a.s ? (int)want : a.s - V;  // s >= V
+    shift = (int)(want - pos);
     return row < rows && i < chunks;
   };
   Chunk<T, V> q[U];

@@ -135,7 +135,7 @@ void cut_last(const deft_norm_desc& d, bool back, NormCut& r) {
       nt = widest(bands) <= 256 ? 256 : deft::kNormThreads;
       ty = nt / widest(bands);
       rounds = 4;
-      const int blocks = ceil_div(d.s, ty * rounds), want = std::max(1, 2 * kCus / std::max(1, d.n * bands));
+      const int blocks = ceil_div(d.s, ty * rounds), want = (int)std::max<int64_t>(1, 2 * kCus / ((int64_t)d.n * bands));
       r.a.rp = std::min(ceil_div(blocks, std::min(blocks, want)), 16) * ty * rounds;
     }
     r.a.slices = ceil_div(d.s, r.a.rp);

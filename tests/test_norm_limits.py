@@ -1,0 +1,80 @@
+"""Group norm at the ends of its range: rows of 2^31 - 1 positions, whose index
+arithmetic passes 32 bits.  The inputs are mostly zeros, so sums in float64 over
+the rest give the values, within the bounds of oracle/norm.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from irregular_gather_cnn_amd.norm import GroupNormAct
+
+H = 2.0 ** -24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["channels_last", "channels_first"])
+@pytest.mark.parametrize("s", [2 ** 31 - 1, 2 ** 31 - 9000])
+def test_rows_of_the_greatest_length(layout, s):
+    """One channel of s positions.  x and dy differ from zero only in the first and last `w` positions,
+    so few values are summed, and every output elsewhere is one known number."""
+    print("norm", layout, s, flush=True)
+    w, guard = 40000, 64
+    assert s > 4 * w
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def row(fill):
+        # 64 elements before and after, so that an access outside the row is seen and stays in memory
+        buf = torch.full((s + 2 * guard,), fill, dtype=torch.bfloat16, device="cuda")
+        return buf, buf[guard:guard + s]
+
+    xb, x = row(0.0)
+    db, dy = row(0.0)
+    for t in (x, dy):
+        t[:w].normal_(generator=gen)
+        t[s - w:].normal_(generator=gen)
+    yb, y = row(7.0)
+    gb, dx = row(7.0)
+    gamma = torch.full((1,), 1.25, dtype=torch.bfloat16, device="cuda")
+    beta = torch.full((1,), 0.25, dtype=torch.bfloat16, device="cuda")
+    shape = (1, s, 1) if layout == "channels_last" else (1, 1, s)
+    h = GroupNormAct(1, 1, s, 1, eps=1e-5, layout=layout, training=True)
+    _, mean, rstd = h.forward(x.view(shape), gamma, beta, y=y.view(shape))
+    out = h.backward(x.view(shape), gamma, beta, mean, rstd, dy.view(shape),
+                     out=dict(dx=dx.view(shape), dgamma=torch.empty_like(gamma), dbeta=torch.empty_like(beta)))
+
+    def ends(t):
+        return torch.cat([t[:w], t[s - w:]]).double().cpu().numpy()
+
+    xe, de = ends(x), ends(dy)
+    m, r = mean.item(), rstd.item()
+    # statistics: fp32 chains of at most 256 in a thread, fp64 beyond
+    want = xe.sum() / s
+    e_mean = 256 * H * np.abs(xe).sum() / s + H * abs(want)
+    assert abs(m - want) <= e_mean
+    var = (xe * xe).sum() / s - want * want
+    assert abs(r - (var + 1e-5) ** -0.5) <= r * (0.5 * 264 * H * var / (var + 1e-5) + 4 * H)
+    # y = 1.25 (x - mean) rstd + 0.25; bf16's rounding, and a few of fp32 before it
+    z = 1.25 * (xe - m) * r + 0.25
+    ez = 8 * H * (1.25 * (np.abs(xe) + abs(m)) * r + 0.25)
+    assert (np.abs(ends(y) - z) <= ez + 2.0 ** -8 * (np.abs(z) + ez)).all()
+    # gradients
+    hh = (xe - m) * r
+    a, b = de.sum(), (de * hh).sum()
+    ea, eb = 256 * H * np.abs(de).sum(), 264 * H * np.abs(de * hh).sum()
+    for got, value, e in ((out["dbeta"], a, ea), (out["dgamma"], b, eb)):
+        assert abs(got.item() - value) <= e + 2.0 ** -8 * (abs(value) + e)
+    d = r * (1.25 * de - 1.25 * a / s - hh * 1.25 * b / s)
+    ed = 16 * H * r * (1.25 * np.abs(de) + 1.25 * abs(a) / s + np.abs(hh) * 1.25 * abs(b) / s) \
+        + r * 1.25 / s * (ea + np.abs(hh) * eb)
+    assert (np.abs(ends(dx) - d) <= ed + 2.0 ** -8 * (np.abs(d) + ed)).all()
+    # between the ends x and dy are zero: one value each, and every position was written
+    for t, value in ((y, 1.25 * (0 - m) * r + 0.25), (dx, r * 1.25 / s * (-a + m * r * b))):
+        mid = t[w:s - w]
+        assert mid.min() == mid.max()
+        if t is dx:
+            e = r * 1.25 / s * (ea + abs(m) * r * eb + 16 * H * (abs(a) + abs(m * r * b)))
+        else:
+            e = 8 * H * (abs(value) + 0.5)
+        assert abs(mid[0].item() - value) <= e + 2.0 ** -8 * (abs(value) + e) + 1e-37
+    for buf, fill in ((yb, 7.0), (gb, 7.0)):
+        assert (buf[:guard] == fill).all() and (buf[guard + s:] == fill).all()
