@@ -313,7 +313,9 @@ int deft_norm_desc_validate(const deft_norm_desc* d);
 /* Bytes of a workspace for deft_norm_forward (training = 0), or for it and
  * deft_norm_backward (training = 1); 0 for a descriptor that they refuse.
  * Zero a workspace before its first call, use it for one descriptor, and order
- * the calls on it: workgroups that share a group count their calls in it. */
+ * the calls on it: workgroups that share a group count their calls in it.  Calls
+ * that break this end all the same; groups whose sums they lose become NaN, and
+ * dgamma and dbeta may be left unwritten. */
 size_t deft_norm_workspace_bytes(const deft_norm_desc* d, int training);
 
 /* How long (ticks of 10 ns; 2 ms at first) a workgroup of either call waits

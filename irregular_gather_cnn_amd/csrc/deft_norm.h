@@ -329,8 +329,12 @@ struct Band {
 // Workgroups wait for each other only up to a deadline.  One that has waited
 // in vain (its peers may not have been started, where other work holds the
 // chip) computes the slices that it misses itself: their values have the same
-// bits whoever computes them.  So every wait ends, and no call depends on how
-// many workgroups are resident.
+// bits whoever computes them.  So no call depends on how many workgroups are
+// resident.  Then all words have been stored, and the last look at them waits
+// for the memory only, as long as calls on a workspace that began with zeros
+// follow each other.  Where they do not, tags of two calls can replace each
+// other for good; so that look has a deadline, too, and what it misses is NaN.
+constexpr uint32_t kLastLook = 1000000;  // ticks: 10 ms, where some microseconds are needed
 struct Joint {
   uint64_t* part;     // [slices][ng][2]
   uint64_t* total;    // [ng][2], where slices * ng is too much for each to read
@@ -353,11 +357,11 @@ struct Joint {
     b = __uint_as_float((uint32_t)v);
     return (uint32_t)(u >> 32) == tag && (uint32_t)(v >> 32) == tag;
   }
-  // Reads until all are there; false at the deadline.
+  // Reads until all are there; false if they were not after the deadline.
   template <typename READ> __device__ __forceinline__ bool wait(READ all) const {
-    while (!all()) {
-      if (__builtin_readsteadycounter() >= deadline) return false;
-      __builtin_amdgcn_s_sleep(1);
+    for (bool late = false; !all(); __builtin_amdgcn_s_sleep(1)) {
+      if (late) return false;
+      late = __builtin_readsteadycounter() >= deadline;
     }
     return true;
   }

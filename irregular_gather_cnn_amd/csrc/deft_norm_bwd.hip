@@ -284,11 +284,15 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(true))) void k_norm_bwd_la
     Joint jt{a.words + (size_t)ng0 * a.slices * 2, a.totals + (size_t)ng0 * 2, tag,
              __builtin_readsteadycounter() + a.patience};
     // groups first, first + step, ... of the band, a wave each
-    auto totals = [&](int first, int every, bool publish) {
+    auto totals = [&](int first, int every, bool publish, bool last) {
       bool ok = true;
       for (int g = first + every * wave; g < w.ng && ok; g += every * waves) {
         float v1, v2;
         ok = sum_joint(a, jt, w.ng, g, v1, v2);
+        if (last && !ok) {
+          v1 = v2 = __builtin_nanf("");
+          ok = true;
+        }
         if (ok && (threadIdx.x & 63) == 0) {
           s1[g] = v1;
           s2[g] = v2;
@@ -304,11 +308,11 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(true))) void k_norm_bwd_la
       sums(slice, [&](int g, float v1, float v2) { jt.publish(slice, w.ng, g, v1, v2); });
       __syncthreads();  // s1 is read above and written below
       if (alone == 2) {
-        totals(0, 1, !a.direct);
+        totals(0, 1, !a.direct, true);
         break;
       }
       if (!alone) {
-        bool ok = a.direct ? totals(0, 1, false) : totals(k, a.slices, true);
+        bool ok = a.direct ? totals(0, 1, false, false) : totals(k, a.slices, true, false);
         if (!a.direct)
           for (int g = threadIdx.x; g < w.ng && ok; g += blockDim.x)
             ok = jt.wait([&] { return jt.read(jt.total + 2 * g, s1[g], s2[g]); });
@@ -320,7 +324,7 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(true))) void k_norm_bwd_la
       if (slice == a.slices) {  // every word has been seen or stored here
         slice = k;
         alone = 2;
-        jt.deadline = ~0ull;
+        jt.deadline = __builtin_readsteadycounter() + kLastLook;
       }
       load(slice);
     }
@@ -514,7 +518,7 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(false))) void k_norm_bwd_f
       sums(s1, s2);
       if (threadIdx.x == 0) jt.publish(slice, 1, 0, s1, s2);
       if (alone == 2) {
-        join();
+        if (!join()) s1 = s2 = __builtin_nanf("");
         break;
       }
       if (!alone) {
@@ -526,7 +530,7 @@ __global__ __launch_bounds__((bound<T, U, MODE, KEEP>(false))) void k_norm_bwd_f
       if (slice == a.slices) {  // every word has been seen or stored here
         slice = k;
         alone = 2;
-        jt.deadline = ~0ull;
+        jt.deadline = __builtin_readsteadycounter() + kLastLook;
       }
       load(slice);
     }

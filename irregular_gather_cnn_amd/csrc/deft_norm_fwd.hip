@@ -270,11 +270,15 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
     __syncthreads();
     Joint jt{a.words + (size_t)ng0 * a.slices * 2, a.totals + (size_t)ng0 * 2, tag, __builtin_readsteadycounter() + a.patience};
     // groups first, first + step, ... of the band, a wave each
-    auto totals = [&](int first, int every, bool publish) {
+    auto totals = [&](int first, int every, bool publish, bool last) {
       bool ok = true;
       for (int g = first + every * wave; g < w.ng && ok; g += every * waves) {
         float mean, rstd;
         ok = combine_joint(a, DEFT_CHANNELS_LAST, jt, w.ng, g, mean, rstd);
+        if (last && !ok) {
+          mean = rstd = __builtin_nanf("");
+          ok = true;
+        }
         if (ok && (threadIdx.x & 63) == 0) {
           gm[g] = mean;
           gr[g] = rstd;
@@ -289,11 +293,11 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
     for (int slice = k, alone = 0;;) {
       statistics([&](int g, float mean, float m2) { jt.publish(slice, w.ng, g, mean, m2); });
       if (alone == 2) {
-        totals(0, 1, !a.direct);
+        totals(0, 1, !a.direct, true);
         break;
       }
       if (!alone) {
-        bool ok = a.direct ? totals(0, 1, false) : totals(k, a.slices, true);
+        bool ok = a.direct ? totals(0, 1, false, false) : totals(k, a.slices, true, false);
         if (!a.direct)
           for (int g = threadIdx.x; g < w.ng && ok; g += blockDim.x)
             ok = jt.wait([&] { return jt.read(jt.total + 2 * g, gm[g], gr[g]); });
@@ -305,7 +309,7 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
       if (slice == a.slices) {  // every word has been seen or stored here
         slice = k;
         alone = 2;
-        jt.deadline = ~0ull;
+        jt.deadline = __builtin_readsteadycounter() + kLastLook;
       }
       load(slice);
     }
@@ -519,7 +523,7 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
       statistics(mean, m2);
       if (threadIdx.x == 0) jt.publish(slice, 1, 0, mean, m2);
       if (alone == 2) {
-        join();
+        if (!join()) mean = rstd = __builtin_nanf("");
         break;
       }
       if (!alone) {
@@ -531,7 +535,7 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
       if (slice == a.slices) {  // every word has been seen or stored here
         slice = k;
         alone = 2;
-        jt.deadline = ~0ull;
+        jt.deadline = __builtin_readsteadycounter() + kLastLook;
       }
       load(slice);
     }

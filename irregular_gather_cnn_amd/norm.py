@@ -26,7 +26,8 @@ class GroupNormAct:
     :meth:`backward` needs too.
 
     Calls run on the device's current stream; calls of one handle on several
-    streams must be ordered by the caller, as they share the workspace."""
+    streams must be ordered by the caller, as they share the workspace (which
+    the constructor zeroes on its current stream)."""
 
     def __init__(self, n, c, s, groups, eps=1e-5, act="none", layout="channels_first", dtype="bf16", training=False,
                  device="cuda"):

@@ -1,7 +1,8 @@
 """Group norm at the ends of its range: rows of 2^31 - 1 positions, whose index
-arithmetic passes 32 bits.  The inputs are mostly zeros, so sums in float64 over
-the rest give the values, within the bounds of oracle/norm.py.
+arithmetic passes 32 bits, and workspaces that were not zeroed.
 """
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -15,7 +16,7 @@ H = 2.0 ** -24
 @pytest.mark.parametrize("layout", ["channels_last", "channels_first"])
 @pytest.mark.parametrize("s", [2 ** 31 - 1, 2 ** 31 - 9000])
 def test_rows_of_the_greatest_length(layout, s):
-    """One channel of s positions.  x and dy differ from zero only in the first and last `w` positions,
+    """One channel of s positions, summed in float64.  x and dy differ from zero only in the first and last `w` positions,
     so few values are summed, and every output elsewhere is one known number."""
     print("norm", layout, s, flush=True)
     w, guard = 40000, 64
@@ -78,3 +79,32 @@ def test_rows_of_the_greatest_length(layout, s):
         assert abs(mid[0].item() - value) <= e + 2.0 ** -8 * (abs(value) + e) + 1e-37
     for buf, fill in ((yb, 7.0), (gb, 7.0)):
         assert (buf[:guard] == fill).all() and (buf[guard + s:] == fill).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["channels_last", "channels_first"])
+@pytest.mark.parametrize("n,c,s,g", [(1, 64, 20001, 1), (2, 40, 9001, 20), (1, 1920, 700, 480)])
+def test_a_workspace_that_was_not_zeroed_ends_every_wait(n, c, s, g, layout):
+    """The counters of calls begin between two calls, so the workgroups of one call carry two numbers and
+    look for words that others replace.  Each element is right or NaN, and the calls end: 24 of them, each
+    with two waits of 2 ms and a last one of 10 ms a workgroup at most, a few workgroups after the other."""
+    print("norm", n, c, s, g, layout, flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    shape = (n, s, c) if layout == "channels_last" else (n, c, s)
+    x, dy = (torch.randn(shape, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    gamma, beta = (torch.randn((c,), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    good = GroupNormAct(n, c, s, g, act="silu", layout=layout, training=True)
+    want = good.forward(x, gamma, beta)
+    back = good.backward(x, gamma, beta, want[1], want[2], dy)
+    h = GroupNormAct(n, c, s, g, act="silu", layout=layout, training=True)
+    torch.cuda.synchronize()
+    start = time.perf_counter()
+    for fill in (1, 2, 3, 7):
+        for _ in range(3):
+            h.ws.view(torch.int64).fill_(fill)
+            got = h.forward(x, gamma, beta)
+            for a, b in zip(got, want):
+                assert ((a == b) | a.isnan()).all()
+            out = h.backward(x, gamma, beta, want[1], want[2], dy)
+            assert ((out["dx"] == back["dx"]) | out["dx"].isnan()).all()
+    assert time.perf_counter() - start < 20
