@@ -328,8 +328,9 @@ void deft_debug_norm_patience(uint32_t ticks);
  * no-op that checks no pointer.
  * DEFT_ERR_BAD_DESC (a negative size, c, eps or enum out of range; y over x),
  * DEFT_ERR_GROUPS (groups < 1 or not a divisor of c), DEFT_ERR_DTYPE,
- * DEFT_ERR_UNSUPPORTED (more than 2048 channels per group, or 2^31 - 1
- * workgroups), DEFT_ERR_NULLPTR, DEFT_ERR_ALIGN (every pointer 16 bytes),
+ * DEFT_ERR_UNSUPPORTED (more than 2048 channels per group; over 2^31 - 1 groups;
+ * a launch of 2^32 threads, which takes over 2^26 - 1 groups of 64 threads or
+ * fewer of more), DEFT_ERR_NULLPTR, DEFT_ERR_ALIGN (every pointer 16 bytes),
  * DEFT_ERR_WORKSPACE; checks run before any launch. */
 int deft_norm_forward(const deft_norm_desc* d, const void* x, const void* gamma, const void* beta, void* y,
                       float* mean, float* rstd, void* workspace, size_t ws_bytes, void* stream);
@@ -400,7 +401,7 @@ typedef struct deft_adamw_tensor {
  * beta2^step, seed} that replace the descriptor's, read when the kernels run:
  * for a captured step whose rates change from replay to replay.
  * DEFT_ERR_DTYPE; DEFT_ERR_BAD_DESC (a negative size, a rate out of range,
- * masters for fp32 weights); DEFT_ERR_UNSUPPORTED (over 2^31 - 1 workgroups of
+ * masters for fp32 weights); DEFT_ERR_UNSUPPORTED (over 2^24 - 1 workgroups of
  * 1024 elements in one tensor); DEFT_ERR_NULLPTR; DEFT_ERR_ALIGN (tensors 16
  * bytes, scales and control 4, schedule 8).  Checks run before any launch. */
 int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int count, const float* control,

@@ -130,6 +130,7 @@ hipError_t launch_backward(const deft_plan& p, const BackwardArgs& a, hipStream_
 // to the device and can be captured; longer lists take several launches.
 constexpr int kStateBlock = DEFT_STATE_BLOCK;  // elements per scale of an 8-bit state
 constexpr int kAdamwElems = 4 * kStateBlock;   // per workgroup
+constexpr int kAdamwThreads = kAdamwElems / 4;
 constexpr int kAdamwList = 50, kNormList = 64; // tensors per launch
 struct AdamwTensor {
   void* p;

@@ -8,6 +8,8 @@
 // So one reduction, over each channel's positions, serves all three gradients.
 // A workgroup holds its slice of x and dy in registers and reads them once;
 // what it keeps is as read, and dz is computed for the sums and again for dx.
+#include <algorithm>
+
 #include "deft_norm.h"
 
 namespace deft {
@@ -591,18 +593,18 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_sums(const NormArgs a, int pa
 }
 
 // dbeta and dgamma: sums of A and B over the rows of part.  16 channels (a line's
-// half) per workgroup, 64 shares of the rows.
+// half) per workgroup, 64 shares of the rows.  `pitch` channels a row, `c` of them here.
 template <typename T>
-__global__ __launch_bounds__(1024) void k_norm_params(const float* __restrict__ part, int rows, int c, T* dgamma,
-                                                      T* dbeta) {
+__global__ __launch_bounds__(1024) void k_norm_params(const float* __restrict__ part, int rows, int pitch, int c,
+                                                      T* dgamma, T* dbeta) {
   __shared__ float lds[2][64][17];
   const int lane = threadIdx.x & 15, ch = blockIdx.x * 16 + lane, share = threadIdx.x >> 4;
   float va = 0.f, vb = 0.f;
   if (ch < c) {
 #pragma unroll 8
     for (int r = share; r < rows; r += 64) {
-      va += part[(size_t)r * 2 * c + ch];
-      vb += part[((size_t)r * 2 + 1) * c + ch];
+      va += part[(size_t)r * 2 * pitch + ch];
+      vb += part[((size_t)r * 2 + 1) * pitch + ch];
     }
   }
   lds[0][share][lane] = va;
@@ -675,16 +677,23 @@ hipError_t launch_norm_bwd_sums(const NormArgs& a, int layout, int dtype, hipStr
   return hipGetLastError();
 }
 
+template <typename T>
+static hipError_t launch_params(const float* part, int rows, int c, T* dgamma, T* dbeta, hipStream_t st) {
+  constexpr int kMost = 1 << 25;  // channels, of 64 threads each: a launch has fewer than 2^32
+  for (int64_t c0 = 0; c0 < c; c0 += kMost) {
+    const int cols = (int)std::min<int64_t>(c - c0, kMost);
+    DEFT_LAUNCH("norm_params", k_norm_params<T>, dim3((cols + 15) / 16), dim3(1024), 0, st, part ? part + c0 : part,
+                rows, c, cols, dgamma ? dgamma + c0 : dgamma, dbeta ? dbeta + c0 : dbeta);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_norm_params(const float* part, int rows, int c, void* dgamma, void* dbeta, int dtype,
                               hipStream_t st) {
-  const dim3 grid((c + 15) / 16);
-  if (dtype == DEFT_BF16)
-    DEFT_LAUNCH("norm_params", k_norm_params<bf16_t>, grid, dim3(1024), 0, st, part, rows, c, (bf16_t*)dgamma,
-                (bf16_t*)dbeta);
-  else
-    DEFT_LAUNCH("norm_params", k_norm_params<float>, grid, dim3(1024), 0, st, part, rows, c, (float*)dgamma,
-                (float*)dbeta);
-  return hipGetLastError();
+  return dtype == DEFT_BF16 ? launch_params(part, rows, c, (bf16_t*)dgamma, (bf16_t*)dbeta, st)
+                            : launch_params(part, rows, c, (float*)dgamma, (float*)dbeta, st);
 }
 
 }  // namespace deft

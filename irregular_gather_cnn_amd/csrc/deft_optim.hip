@@ -28,7 +28,7 @@ namespace deft {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kAdamwThreads;
 constexpr int kPer = 4;                       // consecutive elements per lane: one wave covers a scale's 256
 constexpr int kWaveElems = 64 * kPer;
 constexpr float kCodeMax = 448.f;             // largest e4m3 value

@@ -19,10 +19,12 @@ bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool dtype_ok(int t) { return t == DEFT_F32 || t == DEFT_BF16; }
 int status_of(hipError_t e) { return e == hipSuccess ? DEFT_OK : deft::report_hip_error(e); }
 
-// Workgroups of one launch stay below 2^31.
-constexpr uint64_t kMaxBlocks = 0x7fffffffu;
+// A launch has fewer than 2^32 threads.
+constexpr uint64_t max_blocks(int threads) { return 0xffffffffu / (uint32_t)threads; }
 
-// Gradients of one norm; their pieces stay below 2^31, too.
+constexpr uint64_t kAdamwBlocks = max_blocks(deft::kAdamwThreads);
+
+// Gradients of one norm; their pieces stay below 2^31.
 constexpr uint64_t kMaxElems = 1ull << 44;
 constexpr double kCacheBytes = 256e6;
 
@@ -218,7 +220,11 @@ int norm_cut(const deft_norm_desc& d, bool back, NormCut& r) {
   if (d.layout == DEFT_CHANNELS_LAST) cut_last(d, back, r);
   else cut_first(d, back, r);
   const uint64_t units = (uint64_t)d.n * (d.layout == DEFT_CHANNELS_LAST ? r.a.bands : d.groups);
-  if (units > kMaxBlocks || (uint64_t)d.n * d.groups > kMaxBlocks || units * r.a.slices > kMaxBlocks)
+  // units first: with the slices of one unit, under 2^31, their product stays in 64 bits;
+  // a call that is read twice also has launches of one workgroup a group
+  const uint64_t groups = (uint64_t)d.n * d.groups;  // numbered in 31 bits
+  if (units > max_blocks(r.p.threads) || units * r.a.slices > max_blocks(r.p.threads) || groups > 0x7fffffffu ||
+      (r.mode == deft::kNormStats && groups > max_blocks(back ? 1024 : 256)))
     return DEFT_ERR_UNSUPPORTED;
   r.p.blocks = (uint32_t)(units * r.a.slices);
   return DEFT_OK;
@@ -284,7 +290,7 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
     const deft_adamw_tensor& x = t[i];
     if (x.n < 0 || !(x.weight_decay >= 0.0) || !std::isfinite(x.weight_decay)) return DEFT_ERR_BAD_DESC;
     if (x.n == 0) continue;
-    if (blocks_of(x.n, deft::kAdamwElems) > kMaxBlocks) return DEFT_ERR_UNSUPPORTED;
+    if (blocks_of(x.n, deft::kAdamwElems) > kAdamwBlocks) return DEFT_ERR_UNSUPPORTED;
     if (!x.p || !x.g || !x.m || !x.v || (d->master && !x.master)) return DEFT_ERR_NULLPTR;
     if (d->state_bits == 8 && (!x.m_scale || !x.v_scale)) return DEFT_ERR_NULLPTR;
     if (!aligned16(x.p) || !aligned16(x.g) || !aligned16(x.m) || !aligned16(x.v) ||
@@ -313,7 +319,7 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
   for (int i = 0; i <= count; ++i) {
     const uint64_t more = i < count ? blocks_of(t[i].n, deft::kAdamwElems) : 0;
     // the list is full, or at its end: launch what it holds
-    if (a.count && (i == count || (more && (a.count == deft::kAdamwList || blocks + more > kMaxBlocks)))) {
+    if (a.count && (i == count || (more && (a.count == deft::kAdamwList || blocks + more > kAdamwBlocks)))) {
       const hipError_t e = deft::launch_adamw(a, (uint32_t)blocks, d->p_dtype, d->g_dtype, d->state_bits,
                                               d->master != 0, once, (hipStream_t)stream);
       if (e != hipSuccess) return status_of(e);

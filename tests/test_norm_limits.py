@@ -1,15 +1,54 @@
 """Group norm at the ends of its range: rows of 2^31 - 1 positions, whose index
-arithmetic passes 32 bits, and workspaces that were not zeroed.
+arithmetic passes 32 bits, launches near 2^32 threads, and workspaces that were not zeroed.
 """
+import ctypes
 import time
 
 import numpy as np
 import pytest
 import torch
 
+from irregular_gather_cnn_amd import _lib as L
 from irregular_gather_cnn_amd.norm import GroupNormAct
 
 H = 2.0 ** -24
+
+
+@pytest.mark.parametrize("n,c,s,groups,layout,code", [
+    # a workgroup of 64 threads for each group, or each band of 16: 2^32 threads are too many
+    (2 ** 26 - 1, 1, 1, 1, 0, 0), (2 ** 26, 1, 1, 1, 0, -10), (1, 2 ** 26 - 1, 1, 2 ** 26 - 1, 0, 0),
+    (1, 2 ** 26, 1, 2 ** 26, 0, -10), (2 ** 26 - 1, 1, 1, 1, 1, 0), (2 ** 26, 1, 1, 1, 1, -10),
+    # 31 groups in a band: numbers of groups past 31 bits
+    (2 ** 26 - 1, 31, 1, 31, 1, 0), (2 ** 26 - 1, 62, 1, 62, 1, -10),
+    (2 ** 31 - 1, 1, 1, 1, 0, -10), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 0, -10),
+    # many channels take no more threads than their groups
+    (1, 2 ** 27, 1, 2 ** 16, 0, 0), (1, 2 ** 27, 1, 2 ** 16, 1, 0)])
+def test_launches_stay_below_2_32_threads(n, c, s, groups, layout, code):
+    d = L.deft_norm_desc(n, c, s, groups, layout, 0, L.DEFT_BF16, 1e-5)
+    assert L.load().deft_norm_desc_validate(ctypes.byref(d)) == code
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["channels_last", "channels_first"])
+def test_more_channels_than_one_launch_sums(layout):
+    """2^27 channels in groups of 2048, one position: dbeta = dy and dgamma = dy h, each rounded once."""
+    c, per = 2 ** 27, 2048
+    print("norm", layout, c, flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, dy = (torch.randn((1, c), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    gamma, beta = torch.ones(c, dtype=torch.bfloat16, device="cuda"), torch.zeros(c, dtype=torch.bfloat16, device="cuda")
+    h = GroupNormAct(1, c, 1, c // per, layout=layout, training=True)
+    _, mean, rstd = h.forward(x, gamma, beta)
+    fill = torch.full_like(gamma, 7)
+    out = h.backward(x, gamma, beta, mean, rstd, dy, out=dict(dx=None, dgamma=fill, dbeta=fill.clone()))
+    assert torch.equal(out["dbeta"], dy.view(-1))
+    want = dy.view(-1, per).double() * ((x.view(-1, per).double() - mean.view(-1, 1)) * rstd.view(-1, 1).double())
+    assert ((out["dgamma"].view(-1, per).double() - want).abs() <= want.abs() * (2.0 ** -8 + 8 * H)).all()
+    # no positions: zeros
+    h = GroupNormAct(1, c, 0, c // per, layout=layout, training=True)
+    none = torch.empty((1, c, 0), dtype=torch.bfloat16, device="cuda")
+    out = h.backward(none, gamma, beta, mean, rstd, none, out=dict(dx=None, dgamma=fill, dbeta=fill.clone()))
+    assert not out["dgamma"].any() and not out["dbeta"].any()
 
 
 @pytest.mark.gpu
