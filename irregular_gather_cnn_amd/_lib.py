@@ -134,11 +134,13 @@ def load() -> ctypes.CDLL:
 
 
 def _ptr(t):
+    if t is None or t.__class__ is int:  # addresses, streams: a caught exception takes four times as long
+        return t
     try:
         return t.data_ptr()
     except AttributeError:
         pass
-    if t is None or isinstance(t, int):
+    if isinstance(t, int):
         return t
     if isinstance(t, ctypes.c_void_p):
         return t.value
