@@ -4,11 +4,18 @@ from __future__ import annotations
 import torch
 
 # torch.cuda.current_stream() builds a Stream object for each call, a third of a
-# small operator's time on the host; where torch has the plain getter, that is asked
+# small operator's time on the host; where torch has the plain getters, those are asked
 _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def current_stream(device: torch.device) -> int:
     if _raw is not None and device.index is not None:
         return _raw(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def elsewhere(index: int) -> bool:
+    """Whether GPU `index` is not the current device.  The C ABI launches on the current one: every
+    device's default stream has the handle 0."""
+    return index >= 0 and _device() != index

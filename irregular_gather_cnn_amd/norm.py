@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._stream import current_stream
+from ._stream import current_stream, elsewhere
 
 
 class GroupNormAct:
@@ -25,9 +25,10 @@ class GroupNormAct:
     statistics are float32.  ``training``: hold the workspace that
     :meth:`backward` needs too.
 
-    Calls run on the device's current stream; calls of one handle on several
-    streams must be ordered by the caller, as they share the workspace (which
-    the constructor zeroes on its current stream)."""
+    Calls run on the current stream of their device, whichever device is the
+    current one; calls of one handle on several streams must be ordered by the
+    caller, as they share the workspace (which the constructor zeroes on its
+    current stream)."""
 
     def __init__(self, n, c, s, groups, eps=1e-5, act="none", layout="channels_first", dtype="bf16", training=False,
                  device="cuda"):
@@ -78,6 +79,9 @@ class GroupNormAct:
             mean = torch.empty_like(self._stats)
         if rstd is None:
             rstd = torch.empty_like(self._stats)
+        if elsewhere(self._index):
+            with torch.cuda.device(self._index):
+                return self.forward(x, gamma, beta, y, mean, rstd)
         code = self._forward(self._ref, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(), mean.data_ptr(),
                              rstd.data_ptr(), self._ws, self.ws_bytes, current_stream(self.device))
         if code:
@@ -97,6 +101,9 @@ class GroupNormAct:
             out = dict(dx=torch.empty_like(x), dgamma=torch.empty_like(gamma), dbeta=torch.empty_like(beta))
         else:
             self._refuse(dx=out["dx"], dgamma=out["dgamma"], dbeta=out["dbeta"])
+        if elsewhere(self._index):
+            with torch.cuda.device(self._index):
+                return self.backward(x, gamma, beta, mean, rstd, dy, out)
         dx, dgamma, dbeta = (None if out[k] is None else out[k].data_ptr() for k in ("dx", "dgamma", "dbeta"))
         code = self._backward(self._ref, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), mean.data_ptr(),
                               rstd.data_ptr(), dy.data_ptr(), dx, dgamma, dbeta, self._ws, self.ws_bytes,

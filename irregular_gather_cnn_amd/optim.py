@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._stream import current_stream
+from ._stream import current_stream, elsewhere
 
 _DTYPES = {torch.float32: _lib.DEFT_F32, torch.bfloat16: _lib.DEFT_BF16}
 
@@ -41,7 +41,7 @@ class _Gradients:
             raise ValueError("no gradients")
         self.sizes = [g.numel() for g in self.tensors]
         self.dtype = _dtype_of(self.tensors, "gradients")
-        self.device = self.tensors[0].device
+        self.device, self.index = self.tensors[0].device, self.tensors[0].get_device()
         self.pointers = (ctypes.c_void_p * len(self.sizes))()
         self.bind(self.tensors)
 
@@ -85,6 +85,9 @@ class GradNorm:
 
     def __call__(self, max_norm=float("inf"), inv_scale=1.0):
         g = self.grads
+        if elsewhere(g.index):
+            with torch.cuda.device(g.index):
+                return self(max_norm, inv_scale)
         code = self._call(g.pointers, self._n, len(g.sizes), g.dtype, max_norm, inv_scale, self._out, self._ws,
                           self.ws_bytes, current_stream(g.device))
         if code:
@@ -192,6 +195,9 @@ class AdamW:
                 if t is not None and (t.numel() != 4 or t.dtype != kind or t.device != self.device
                                       or not t.is_contiguous()):
                     raise ValueError("%s must be 4 contiguous elements of %s on %s" % (what, kind, self.device))
+        if elsewhere(self.grads.index):
+            with torch.cuda.device(self.grads.index):
+                return self.step(control, lr, schedule)
         d = self._desc
         d.lr, d.step, d.seed = self.lr, self.steps + 1, self.step_seed(self.steps + 1)
         code = self._call(self._ref, self._list, len(self.params), None if control is None else control.data_ptr(),
