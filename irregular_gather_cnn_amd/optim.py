@@ -31,6 +31,12 @@ def _dense(t, what, device=None):
     return t
 
 
+def _hold(tensors):
+    """The memory of these tensors, for as long as its addresses are in use, also where a program gives
+    a tensor other memory (``t.data = ...``)."""
+    return [t.detach() for t in tensors if t is not None]
+
+
 class _Gradients:
     """The gradient buffers of a program: their sizes and dtype for good, the
     buffers themselves until :meth:`bind` names others."""
@@ -53,7 +59,7 @@ class _Gradients:
             if g.numel() != n or _DTYPES.get(g.dtype) != self.dtype:
                 raise ValueError("gradient %d must have %d elements of the dtype of the first ones" % (k, n))
             _dense(g, "gradient %d" % k, self.device)
-        self.tensors = grads
+        self.tensors, self.held = grads, _hold(grads)
         for k, g in enumerate(grads):
             self.pointers[k] = g.data_ptr()
 
@@ -106,7 +112,11 @@ class AdamW:
     a list of fp32 tensors.  ``weight_decay``: one number or one per tensor.
     ``states``: None (zeros) or a list of (m, v, m_scale, v_scale) per param,
     updated in place (the scales None with 32 bits), as :attr:`states` of an
-    earlier run whose :attr:`steps` is passed as ``step``."""
+    earlier run whose :attr:`steps` is passed as ``step``.
+
+    The addresses of all tensors are taken here and in :meth:`bind`, and that
+    memory is held: a tensor that is given other memory later on (``p.data =
+    ...``) needs a new handle, a gradient a new :meth:`bind`."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32,
                  masters=None, states=None, step=0, seed=0):
@@ -144,6 +154,7 @@ class AdamW:
                 p.data_ptr(), self.grads.pointers[k], m.data_ptr(), v.data_ptr(), ms.data_ptr() if bits == 8 else None,
                 vs.data_ptr() if bits == 8 else None, self.masters[k].data_ptr() if self.masters else None,
                 self.sizes[k], decay[k])
+        self._held = _hold(self.params + (self.masters or []) + [t for s in self.states for t in s])
         self._call, self._ref = _lib.load().deft_adamw_step, ctypes.byref(self._desc)
         self._norm = GradNorm.__new__(GradNorm)
         self._norm._setup(self.grads)

@@ -1,8 +1,11 @@
-"""AdamW at the ends of its range: launches have fewer than 2^32 threads, of 1024 elements a 256."""
+"""AdamW at the ends of its range: launches have fewer than 2^32 threads, of 1024 elements a 256; and the
+memory that its handles point to."""
+import gc
+
 import pytest
 import torch
 
-from irregular_gather_cnn_amd.optim import AdamW
+from irregular_gather_cnn_amd.optim import AdamW, GradNorm
 from test_optim import FAKE, step_call
 
 MOST = (2 ** 24 - 1) * 1024  # elements of one launch
@@ -36,3 +39,19 @@ def test_a_list_of_more_than_one_launch():
     for t in run(sizes):
         assert t.min() == t.max() == want
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_handles_hold_the_memory_they_point_to(bits):
+    """Also where every tensor of the program gets other memory."""
+    sizes = [300, 7]
+    p, g = ([torch.zeros(n, dtype=torch.bfloat16) for n in sizes] for _ in range(2))
+    opt, norm = AdamW(p, g, bits=bits, masters=True), GradNorm(g)
+    for t in p + g + opt.masters + [t for s in opt.states for t in s if t is not None]:
+        t.data = torch.empty_like(t)
+    gc.collect()
+    kept = {t.data_ptr() for t in gc.get_objects() if type(t) is torch.Tensor}
+    for item in opt._list:
+        for field in ("p", "g", "m", "v", "master") + (("m_scale", "v_scale") if bits == 8 else ()):
+            assert getattr(item, field) in kept, field
+    assert set(norm.grads.pointers) <= kept
