@@ -332,12 +332,9 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
     be[j] = bet[w.col - w.c0 + j];
     if (--next == 0) { next = per; ++gi; }
   }
-  // bf16: z in one operation from x; its error, a rounding of mean * gamma * rstd,
-  // is far below y's own where bf16 can tell x from its mean at all
-  if (sizeof(T) == 2) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) be[j] = __builtin_fmaf(-mu[j], ga[j], be[j]);
-  }
+  // z from x - mean, as the backward computes it: with the mean in the bias, the
+  // rounding of mean * gamma * rstd would stay, 0.006 in a constant group of 1000s,
+  // whose z is beta
   T* yp = (T*)a.out + at;
   with_act(a.act, [&](auto act) {
     T* p = yp;
@@ -350,8 +347,7 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
         q[u].get(f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = sizeof(T) == 2 ? f[j] : f[j] - mu[j];
-          f[j] = act_of<T, decltype(act)::value>(__builtin_fmaf(d, ga[j], be[j]));
+          f[j] = act_of<T, decltype(act)::value>(__builtin_fmaf(f[j] - mu[j], ga[j], be[j]));
         }
         Chunk<T, V>::store(p, f);
         p += step;
@@ -554,15 +550,13 @@ __global__ __launch_bounds__(kNormThreads, MODE == kNormJoint ? 4 : 1) void k_no
       int pos, shift;
       const bool ok = slot(row, i, pos, shift);
       if (u < rounds && ok) {
-        const float ga = gam[row] * rstd;
-        const float be = sizeof(T) == 2 ? __builtin_fmaf(-mean, ga, bet[row]) : bet[row];  // as above
+        const float ga = gam[row] * rstd, be = bet[row];
         float f[V];
         q[u].keep();
         q[u].get(f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = sizeof(T) == 2 ? f[j] : f[j] - mean;
-          f[j] = act_of<T, decltype(act)::value>(__builtin_fmaf(d, ga, be));
+          f[j] = act_of<T, decltype(act)::value>(__builtin_fmaf(f[j] - mean, ga, be));
         }
         Chunk<T, V>::store(yp + (size_t)row * a.s + pos, f);
       }
