@@ -315,12 +315,22 @@ typedef struct deft_norm_desc {
 int deft_norm_desc_validate(const deft_norm_desc* d);
 
 /* Bytes of a workspace for deft_norm_forward (training = 0), or for it and
- * deft_norm_backward (training = 1); 0 for a descriptor that they refuse.
+ * deft_norm_backward (training = 1); 0 for a descriptor that they refuse.  It
+ * and the calls look at the current device, which must be the same for all.
  * Zero a workspace before its first call, use it for one descriptor, and order
  * the calls on it: workgroups that share a group count their calls in it.  Calls
  * that break this end all the same; groups whose sums they lose become NaN, and
  * dgamma and dbeta may be left unwritten. */
 size_t deft_norm_workspace_bytes(const deft_norm_desc* d, int training);
+
+/* How the forward (back = 0) or the backward (1) cuts a descriptor with
+ * elements, on a device of `cus` compute units (0: those of the current one):
+ * cut[8] = {form: 0 one workgroup a group, 1 several that exchange their sums, 2
+ * read twice; elements per access; accesses per thread; threads per workgroup;
+ * workgroups that share a group (a band of groups); workgroups; whether each of
+ * them reads all exchanged words; cus}.  For tests.  Errors as for
+ * deft_norm_desc_validate; DEFT_ERR_BAD_DESC for no elements. */
+int deft_debug_norm_cut(const deft_norm_desc* d, int back, int cus, int* cut);
 
 /* How long (ticks of 10 ns; 2 ms at first) a workgroup of either call waits
  * for the others that share its group, before it computes their sums itself;

@@ -30,7 +30,7 @@ EXPORTED = ["deft_desc_validate", "deft_plan_create", "deft_plan_create_forced",
             "deft_timing_get", "deft_dwconv1d_forward", "deft_dwpw1d_forward",
             "deft_adamw_step", "deft_grad_norm", "deft_grad_norm_workspace_bytes",
             "deft_norm_desc_validate", "deft_norm_workspace_bytes", "deft_norm_forward",
-            "deft_norm_backward", "deft_debug_norm_patience"]
+            "deft_norm_backward", "deft_debug_norm_patience", "deft_debug_norm_cut"]
 LAYOUTS = {"channels_first": 0, "channels_last": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
@@ -115,6 +115,7 @@ def load() -> ctypes.CDLL:
         "deft_grad_norm_workspace_bytes": (sz, [i]),
         "deft_norm_desc_validate": (i, [ctypes.POINTER(deft_norm_desc)]),
         "deft_norm_workspace_bytes": (sz, [ctypes.POINTER(deft_norm_desc), i]),
+        "deft_debug_norm_cut": (i, [ctypes.POINTER(deft_norm_desc), i, i, vp]),
         "deft_debug_norm_patience": (None, [ctypes.c_uint32]),
         "deft_norm_forward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 7 + [sz, vp]),
         "deft_norm_backward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 10 + [sz, vp]),
@@ -278,6 +279,15 @@ def deft_norm_desc_validate(desc: deft_norm_desc) -> None:
 
 def deft_norm_workspace_bytes(desc: deft_norm_desc, training: int) -> int:
     return int(load().deft_norm_workspace_bytes(ctypes.byref(desc), int(training)))
+
+
+NORM_CUT = ("form", "vec", "accesses", "threads", "slices", "blocks", "direct", "cus")
+
+
+def deft_debug_norm_cut(desc: deft_norm_desc, back: bool, cus: int = 0) -> dict:
+    cut = (ctypes.c_int * len(NORM_CUT))()
+    _check(load().deft_debug_norm_cut(ctypes.byref(desc), int(back), int(cus), cut), "deft_debug_norm_cut")
+    return dict(zip(NORM_CUT, cut))
 
 
 def deft_debug_norm_patience(ticks: int) -> None:

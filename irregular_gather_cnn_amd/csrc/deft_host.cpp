@@ -467,6 +467,7 @@ thread_local Timing g_timing;
 
 namespace deft {
 int report_hip_error(hipError_t e) { return hip_fail(e); }
+int compute_units() { return device_limits().cus; }
 
 void timing_before(hipStream_t s, const char* name) {
   Timing& t = g_timing;

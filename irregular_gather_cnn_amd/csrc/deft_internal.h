@@ -54,6 +54,8 @@ inline bool woff_a16(int dtype, int oc, int wo) { return dtype == DEFT_BF16 && o
 
 // Records a HIP error for deft_last_hip_error and returns DEFT_ERR_HIP.
 int report_hip_error(hipError_t e);
+// Of the current device; 256 where there is none.
+int compute_units();
 
 // Timing hook (deft_timing_start): brackets a launch with events when active.
 void timing_before(hipStream_t s, const char* name);

@@ -36,7 +36,6 @@ int norm_launches(int count) { return std::max(1, (count + deft::kNormList - 1) 
 // ---- group norm: how a call is cut ----
 
 constexpr int kMaxPer = 2048;      // channels per group: a row of one group fits a workgroup
-constexpr int kCus = 256;
 constexpr size_t kAlign = 256;
 
 size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
@@ -58,11 +57,12 @@ struct NormCut {
   deft::NormArgs a;
   deft::NormPlan p;
   int mode;  // kNormWhole, kNormJoint, or kNormStats: statistics, then a second launch
+  int cus;   // compute units of the device that it is cut for
 };
 
 // Workgroups of `threads` that the chip holds at once: the forward's joint
 // kernels take up to 128 registers, the backward's up to 256.
-int resident(bool back, int threads) { return kCus * (back ? 512 : 1024) / threads; }
+int resident(const NormCut& r, bool back, int threads) { return r.cus * (back ? 512 : 1024) / threads; }
 
 // One slice for a group (or a band of groups), where it fits the registers:
 // 32 accesses a thread forward, 16 of x and of dy backward.  It needs no
@@ -73,9 +73,9 @@ int resident(bool back, int threads) { return kCus * (back ? 512 : 1024) / threa
 // (us in one slice and joined): 12 bands of 9000 elements, gelu fp32, 8.6 and 10.7;
 // 5 groups of 20252, relu bf16, 6.1 and 7.1; 10 of 43590, none bf16, 10.2 and 8.6; 50
 // of 42476, none fp32, 18.7 and 10.9.
-bool whole_pays(const deft_norm_desc& d, bool back, int V, int rounds, int64_t units, int64_t elems) {
+bool whole_pays(const deft_norm_desc& d, const NormCut& r, bool back, int V, int rounds, int64_t units, int64_t elems) {
   if (rounds > (V == 1 || back ? 16 : 32)) return false;
-  if (units >= kCus * 3 / 4) return true;
+  if (units >= r.cus * 3 / 4) return true;
   const int act = d.act == DEFT_ACT_GELU ? 40 : d.act == DEFT_ACT_SILU ? 24 : 12;
   const int bytes = d.dtype == DEFT_F32 ? 52 : 26;
   if (back) return elems * std::max(2 * act, bytes * 3 / 2) <= 1000000;
@@ -120,14 +120,14 @@ void cut_last(const deft_norm_desc& d, bool back, NormCut& r) {
   r.mode = deft::kNormWhole;
   r.a.slices = 1;
   r.a.rp = d.s;
-  if (!whole_pays(d, back, V, rounds, (int64_t)d.n * bands, (int64_t)ceil_div(g, bands) * per * d.s)) {
+  if (!whole_pays(d, r, back, V, rounds, (int64_t)d.n * bands, (int64_t)ceil_div(g, bands) * per * d.s)) {
     bands = ceil_div(g, std::max(1, 1024 / per));
     nt = back && widest(bands) <= 256 ? 256 : deft::kNormThreads;
     int ty = nt / widest(bands);
     rounds = 8;
     auto slices = [&] { return ceil_div(d.s, (int64_t)ty * rounds); };
-    while (rounds > 4 && (int64_t)d.n * bands * slices() < kCus) rounds /= 2;
-    const bool joint = (int64_t)d.n * d.s * d.c < 1 << 21 && slices() <= resident(back, nt);
+    while (rounds > 4 && (int64_t)d.n * bands * slices() < r.cus) rounds /= 2;
+    const bool joint = (int64_t)d.n * d.s * d.c < 1 << 21 && slices() <= resident(r, back, nt);
     r.mode = joint ? deft::kNormJoint : deft::kNormStats;
     r.a.rp = ty * rounds;
     if (back && r.mode == deft::kNormStats) {
@@ -137,7 +137,7 @@ void cut_last(const deft_norm_desc& d, bool back, NormCut& r) {
       nt = widest(bands) <= 256 ? 256 : deft::kNormThreads;
       ty = nt / widest(bands);
       rounds = 4;
-      const int blocks = ceil_div(d.s, ty * rounds), want = (int)std::max<int64_t>(1, 2 * kCus / ((int64_t)d.n * bands));
+      const int blocks = ceil_div(d.s, ty * rounds), want = (int)std::max<int64_t>(1, 2 * r.cus / ((int64_t)d.n * bands));
       r.a.rp = std::min(ceil_div(blocks, std::min(blocks, want)), 16) * ty * rounds;
     }
     r.a.slices = ceil_div(d.s, r.a.rp);
@@ -188,12 +188,12 @@ void cut_first(const deft_norm_desc& d, bool back, NormCut& r) {
   r.a.rp = per;
   r.a.ws = 1;
   r.a.cp = d.s;
-  if (!whole_pays(d, back, V, rounds, (int64_t)d.n * d.groups, (int64_t)per * d.s)) {
+  if (!whole_pays(d, r, back, V, rounds, (int64_t)d.n * d.groups, (int64_t)per * d.s)) {
     nt = back ? 256 : deft::kNormThreads;
     int cpc = ceil_div(chunks, ceil_div(chunks, nt * 4));  // chunks of a channel in a slice
     int rp = std::min(per, std::max(1, nt * 8 / cpc));
     auto slices = [&] { return (int64_t)ceil_div(per, rp) * ceil_div(chunks, cpc); };
-    while ((int64_t)d.n * d.groups * slices() < kCus && rp * (int64_t)cpc > nt * 4) {
+    while ((int64_t)d.n * d.groups * slices() < r.cus && rp * (int64_t)cpc > nt * 4) {
       if (rp > 1) rp = (rp + 1) / 2;
       else cpc = (cpc + 1) / 2;
     }
@@ -201,7 +201,7 @@ void cut_first(const deft_norm_desc& d, bool back, NormCut& r) {
     r.a.rp = rp;
     r.a.cp = cpc * V;
     r.a.ws = ceil_div(chunks, cpc);
-    r.mode = slices() <= resident(back, nt) ? deft::kNormJoint : deft::kNormStats;
+    r.mode = slices() <= resident(r, back, nt) ? deft::kNormJoint : deft::kNormStats;
     r.a.direct = 1;
   }
   r.a.slices = ceil_div(per, r.a.rp) * r.a.ws;
@@ -211,8 +211,9 @@ void cut_first(const deft_norm_desc& d, bool back, NormCut& r) {
   r.p.lds = sizeof(float) * (back ? std::max(2 * nt, 32 + (2 + 2 * subs) * r.a.rp) : 32 + 2 * r.a.rp);
 }
 
-int norm_cut(const deft_norm_desc& d, bool back, NormCut& r) {
+int norm_cut(const deft_norm_desc& d, bool back, NormCut& r, int cus = deft::compute_units()) {
   std::memset(&r, 0, sizeof(r));
+  r.cus = cus;
   r.a.n = d.n; r.a.c = d.c; r.a.s = d.s; r.a.g = d.groups;
   r.a.per = d.c / d.groups;
   r.a.act = d.act;
@@ -414,6 +415,19 @@ size_t deft_norm_workspace_bytes(const deft_norm_desc* d, int training) {
   const size_t fwd = norm_layout(*d, false, f, nullptr);
   if (!training) return fwd;
   return norm_cut(*d, true, b) == DEFT_OK ? fwd + norm_layout(*d, true, b, nullptr) : 0;
+}
+
+int deft_debug_norm_cut(const deft_norm_desc* d, int back, int cus, int* cut) {
+  const int st = norm_desc_status(d);
+  if (st != DEFT_OK) return st;
+  if (!cut) return DEFT_ERR_NULLPTR;
+  if (cus < 0 || d->n == 0 || d->s == 0) return DEFT_ERR_BAD_DESC;
+  NormCut r;
+  const int e = norm_cut(*d, back != 0, r, cus ? cus : deft::compute_units());
+  if (e != DEFT_OK) return e;
+  const int out[8] = {r.mode, r.p.vec, r.p.u, r.p.threads, r.a.slices, (int)r.p.blocks, r.a.direct, r.cus};
+  std::memcpy(cut, out, sizeof(out));
+  return DEFT_OK;
 }
 
 void deft_debug_norm_patience(uint32_t ticks) { g_patience = ticks; }

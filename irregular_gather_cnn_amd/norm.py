@@ -6,6 +6,7 @@ in ``_lib``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -38,13 +39,14 @@ class GroupNormAct:
                 raise ValueError("%s must be one of %s, got %r" % (what, sorted(known), value))
         self.desc = _lib.deft_norm_desc(n, c, s, groups, _lib.LAYOUTS[layout], _lib.ACTIVATIONS[act],
                                         _lib.DEFT_BF16 if dtype == "bf16" else _lib.DEFT_F32, eps)
-        _lib.deft_norm_desc_validate(self.desc)
+        self._index = torch.empty(0, device=device).get_device()
+        with torch.cuda.device(self._index) if elsewhere(self._index) else contextlib.nullcontext():
+            _lib.deft_norm_desc_validate(self.desc)
+            self.ws_bytes = _lib.deft_norm_workspace_bytes(self.desc, 1 if training else 0)
         self.n, self.c, self.s, self.groups = n, c, s, groups
         self.tdtype, self.training = _DTYPES[dtype], training
-        self.ws_bytes = _lib.deft_norm_workspace_bytes(self.desc, 1 if training else 0)
         self.ws = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
         self.device = self.ws.device
-        self._index = self.ws.get_device()
         self._stats = torch.empty((n, groups), dtype=torch.float32, device=device)
         # what each argument must be: elements and dtype
         self._image, self._channel, self._stat = (n * c * s, self.tdtype), (c, self.tdtype), (n * groups, torch.float32)
