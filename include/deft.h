@@ -339,7 +339,7 @@ void deft_debug_norm_patience(uint32_t ticks);
 
 /* y = act(group norm of x), and mean and rstd (fp32 [n][groups], written) as
  * deft_norm_backward takes them.  y must not overlap x.  n = 0 or s = 0 is a
- * no-op that checks no pointer.
+ * no-op that checks no pointer and writes nothing.
  * DEFT_ERR_BAD_DESC (a negative size, c, eps or enum out of range; y over x),
  * DEFT_ERR_GROUPS (groups < 1 or not a divisor of c), DEFT_ERR_DTYPE,
  * DEFT_ERR_UNSUPPORTED (more than 2048 channels per group; over 2^31 - 1 groups;

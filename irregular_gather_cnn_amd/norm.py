@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 
 import torch
 
@@ -69,7 +70,7 @@ class GroupNormAct:
                     (what,) + self._kinds[what] + (self.device,)))
 
     def forward(self, x, gamma, beta, y=None, mean=None, rstd=None):
-        """(y, mean, rstd); mean and rstd are float32 [n][groups]."""
+        """(y, mean, rstd); mean and rstd are float32 [n][groups], NaN where there are no positions."""
         unfit = self._unfit
         if unfit(x, self._image) or unfit(gamma, self._channel) or unfit(beta, self._channel):
             self._refuse(x=x, gamma=gamma, beta=beta)
@@ -81,6 +82,9 @@ class GroupNormAct:
             mean = torch.empty_like(self._stats)
         if rstd is None:
             rstd = torch.empty_like(self._stats)
+        if self.s == 0:  # the C function writes nothing, then
+            mean.fill_(math.nan)
+            rstd.fill_(math.nan)
         if elsewhere(self._index):
             with torch.cuda.device(self._index):
                 return self.forward(x, gamma, beta, y, mean, rstd)

@@ -147,3 +147,15 @@ def test_a_workspace_that_was_not_zeroed_ends_every_wait(n, c, s, g, layout):
             out = h.backward(x, gamma, beta, want[1], want[2], dy)
             assert ((out["dx"] == back["dx"]) | out["dx"].isnan()).all()
     assert time.perf_counter() - start < 20
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+def test_no_positions_have_no_statistics(given):
+    x, c = torch.empty(3, 8, 0, device="cuda"), torch.ones(8, device="cuda")
+    h = GroupNormAct(3, 8, 0, 2, dtype="f32")
+    torch.full((3, 2), 5.0, device="cuda")  # what memory that is not written is likely to hold
+    out = dict(mean=torch.ones(3, 2, device="cuda"), rstd=torch.ones(3, 2, device="cuda")) if given else {}
+    y, mean, rstd = h.forward(x, c, c, **out)
+    assert y.shape == x.shape and mean.shape == rstd.shape == (3, 2)
+    assert mean.isnan().all() and rstd.isnan().all()
