@@ -96,7 +96,7 @@ class GroupNormAct:
 
     def backward(self, x, gamma, beta, mean, rstd, dy, out=None):
         """dict(dx, dgamma, dbeta).  ``out``: the buffers to write; what it
-        holds as None is not computed."""
+        leaves out or holds as None is not computed."""
         if not self.training:
             raise ValueError("backward needs training=True")
         unfit = self._unfit
@@ -106,11 +106,13 @@ class GroupNormAct:
         if out is None:
             out = dict(dx=torch.empty_like(x), dgamma=torch.empty_like(gamma), dbeta=torch.empty_like(beta))
         else:
-            self._refuse(dx=out["dx"], dgamma=out["dgamma"], dbeta=out["dbeta"])
+            if not out.keys() <= _GRADIENTS:
+                raise ValueError("out may hold %s, got %s" % (sorted(_GRADIENTS), sorted(out)))
+            self._refuse(**out)
         if elsewhere(self._index):
             with torch.cuda.device(self._index):
                 return self.backward(x, gamma, beta, mean, rstd, dy, out)
-        dx, dgamma, dbeta = (None if out[k] is None else out[k].data_ptr() for k in ("dx", "dgamma", "dbeta"))
+        dx, dgamma, dbeta = (None if out.get(k) is None else out[k].data_ptr() for k in ("dx", "dgamma", "dbeta"))
         code = self._backward(self._ref, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), mean.data_ptr(),
                               rstd.data_ptr(), dy.data_ptr(), dx, dgamma, dbeta, self._ws, self.ws_bytes,
                               current_stream(self.device))
@@ -119,4 +121,5 @@ class GroupNormAct:
         return out
 
 
+_GRADIENTS = {"dx", "dgamma", "dbeta"}
 _DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}

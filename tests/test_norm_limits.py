@@ -159,3 +159,27 @@ def test_no_positions_have_no_statistics(given):
     y, mean, rstd = h.forward(x, c, c, **out)
     assert y.shape == x.shape and mean.shape == rstd.shape == (3, 2)
     assert mean.isnan().all() and rstd.isnan().all()
+
+
+def test_backward_refuses_unknown_buffers_before_any_launch():
+    x, c, st = torch.zeros(2, 8, 4), torch.ones(8), torch.zeros(2, 2)
+    h = GroupNormAct(2, 8, 4, 2, dtype="f32", training=True, device="cpu")
+    with pytest.raises(ValueError, match="dw"):
+        h.backward(x, c, c, st, st, x, out=dict(dx=x.clone(), dw=c))
+    with pytest.raises(ValueError, match="dgamma"):
+        h.backward(x, c, c, st, st, x, out=dict(dgamma=x))
+
+
+@pytest.mark.gpu
+def test_backward_writes_the_buffers_it_is_given():
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, dy = (torch.randn((2, 8, 40), generator=gen, device="cuda") for _ in range(2))
+    c = torch.randn((8,), generator=gen, device="cuda")
+    h = GroupNormAct(2, 8, 40, 2, act="silu", dtype="f32", training=True)
+    _, mean, rstd = h.forward(x, c, c)
+    want = h.backward(x, c, c, mean, rstd, dy)
+    for keep in (("dx",), ("dgamma", "dbeta"), ("dbeta",), ()):
+        out = h.backward(x, c, c, mean, rstd, dy, out={k: torch.zeros_like(want[k]) for k in keep})
+        assert sorted(out) == sorted(keep)
+        for k in keep:
+            assert torch.equal(out[k], want[k])
