@@ -2,6 +2,8 @@
 
 Every function keeps the C name and signature; device pointers may be passed
 as torch tensors (their ``data_ptr()``), plain integers or ``None`` (NULL).
+The training operators' calls, whose small cases wait for the host, go to the
+library's own functions (``load().deft_norm_forward``) from their classes.
 A non-zero status raises :class:`DeftError`.  Nothing here computes any part
 of the layer: all of it runs in the HIP library, and loading fails loudly if
 the library has not been built.
@@ -257,18 +259,6 @@ def deft_halo_histogram(desc: deft_desc, offsets, hist, hist_len: int, stream=No
                                       _ptr(stream)), "deft_halo_histogram")
 
 
-def deft_adamw_step(desc: deft_adamw_desc, tensors, count, control=None, schedule=None, stream=None) -> None:
-    """tensors: a ctypes array of deft_adamw_tensor (host)."""
-    _check(load().deft_adamw_step(ctypes.byref(desc), tensors, int(count), _ptr(control), _ptr(schedule),
-                                  _ptr(stream)), "deft_adamw_step")
-
-
-def deft_grad_norm(g, n, count, g_dtype, max_norm, inv_scale, control, workspace, ws_bytes, stream=None) -> None:
-    """g, n: ctypes arrays of c_void_p and c_int64 (host)."""
-    _check(load().deft_grad_norm(g, n, int(count), int(g_dtype), float(max_norm), float(inv_scale), _ptr(control),
-                                 _ptr(workspace), int(ws_bytes), _ptr(stream)), "deft_grad_norm")
-
-
 def deft_grad_norm_workspace_bytes(count: int) -> int:
     return int(load().deft_grad_norm_workspace_bytes(int(count)))
 
@@ -292,18 +282,6 @@ def deft_debug_norm_cut(desc: deft_norm_desc, back: bool, cus: int = 0) -> dict:
 
 def deft_debug_norm_patience(ticks: int) -> None:
     load().deft_debug_norm_patience(int(ticks))
-
-
-def deft_norm_forward(desc: deft_norm_desc, x, gamma, beta, y, mean, rstd, workspace, ws_bytes, stream=None) -> None:
-    _check(load().deft_norm_forward(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
-                                    _ptr(rstd), _ptr(workspace), int(ws_bytes), _ptr(stream)), "deft_norm_forward")
-
-
-def deft_norm_backward(desc: deft_norm_desc, x, gamma, beta, mean, rstd, dy, dx, dgamma, dbeta, workspace, ws_bytes,
-                       stream=None) -> None:
-    _check(load().deft_norm_backward(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
-                                     _ptr(dy), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), int(ws_bytes),
-                                     _ptr(stream)), "deft_norm_backward")
 
 
 def deft_error_string(code: int) -> str:
