@@ -380,6 +380,7 @@ typedef struct deft_adamw_desc {
   int64_t step;         /* this step's number, from 1 */
   double lr, beta1, beta2, eps; /* lr, eps >= 0; 0 <= beta < 1 */
   uint32_t seed;        /* 8-bit states: a new one for each step */
+  uint32_t* skipped;    /* device, may be NULL: how many steps control has skipped, 0 at first */
 } deft_adamw_desc;
 
 typedef struct deft_adamw_tensor {
@@ -410,14 +411,17 @@ typedef struct deft_adamw_tensor {
  * start in both forms.
  * control (device, may be NULL): what deft_grad_norm wrote.  Its factor
  * multiplies the gradients; if it says that they are not finite, the step
- * writes nothing.
+ * writes nothing, but adds 1 to desc.skipped.
+ * desc.skipped: a step's number in 1 - beta^step is desc.step less this count, so
+ * skipped steps leave no mark on later ones, without a copy to the host.  Without
+ * it, or with a schedule, they count as steps.
  * schedule (device, may be NULL): 4 doubles {lr, 1 - beta1^step, 1 -
  * beta2^step, seed} that replace the descriptor's, read when the kernels run:
  * for a captured step whose rates change from replay to replay.
  * DEFT_ERR_DTYPE; DEFT_ERR_BAD_DESC (a negative size, a rate out of range,
  * masters for fp32 weights); DEFT_ERR_UNSUPPORTED (over 2^24 - 1 workgroups of
  * 1024 elements in one tensor); DEFT_ERR_NULLPTR; DEFT_ERR_ALIGN (tensors 16
- * bytes, scales and control 4, schedule 8).  Checks run before any launch. */
+ * bytes, scales, control and skipped 4, schedule 8).  Checks run before any launch. */
 int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int count, const float* control,
                     const double* schedule, void* stream);
 

@@ -67,7 +67,7 @@ class deft_adamw_desc(ctypes.Structure):
     _fields_ = [("p_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int), ("state_bits", ctypes.c_int),
                 ("master", ctypes.c_int), ("step", ctypes.c_int64), ("lr", ctypes.c_double),
                 ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
-                ("seed", ctypes.c_uint32)]
+                ("seed", ctypes.c_uint32), ("skipped", ctypes.c_void_p)]
 
 
 class deft_adamw_tensor(ctypes.Structure):

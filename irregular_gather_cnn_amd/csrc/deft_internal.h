@@ -149,11 +149,15 @@ struct AdamwArgs {
   AdamwTensor t[kAdamwList];
   uint32_t first[kAdamwList];  // first workgroup of each tensor
   uint32_t id[kAdamwList];     // its number in the call's list
-  int count;
+  uint16_t count;
+  uint16_t lead;           // the call's first launch, which counts a skipped step
   float b1, c1, b2, c2, eps, rate, low;
   uint32_t seed;
   const float* control;    // nullable
   const double* schedule;  // nullable
+  uint32_t* skipped;       // nullable; where it is above 0, rate and low are computed from:
+  double lr, log1, log2;   // log2 of beta1 and beta2
+  int64_t step;
 };
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
 hipError_t launch_adamw(const AdamwArgs& a, uint32_t blocks, int p_dtype, int g_dtype, int bits, bool master,

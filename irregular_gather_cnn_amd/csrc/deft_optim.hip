@@ -200,10 +200,28 @@ __device__ __forceinline__ void adamw(float g, float& m, float& v, float& root, 
 template <typename P, typename G, int BITS, bool MASTER, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwArgs a) {
 #pragma clang fp contract(off)
+  const uint32_t skipped = a.skipped ? *a.skipped : 0;
   float coef = 1.f;
   if (a.control) {
     coef = a.control[1];
-    if (a.control[2] == 0.f) return;  // gradients not finite: nothing is written
+    if (a.control[2] == 0.f) {  // gradients not finite: the step is counted, and nothing else is written
+      if (a.skipped && a.lead && blockIdx.x == 0 && threadIdx.x == 0) *a.skipped = skipped + 1;
+      return;
+    }
+  }
+  Rates r{a.b1, a.c1, a.b2, a.c2, a.eps, a.rate, a.low};
+  if (skipped && !a.schedule) {
+    // The corrections of the steps that were taken.  A wave's work for the workgroup: in every wave, these
+    // fp64 operations would take as long as a third of the step's memory accesses.
+    __shared__ float corrected[2];
+    if (threadIdx.x < 64) {
+      const double taken = (double)(a.step > skipped ? a.step - skipped : 1);
+      corrected[0] = (float)(a.lr / (1.0 - exp2(taken * a.log1)));
+      corrected[1] = (float)(1.0 / sqrt(1.0 - exp2(taken * a.log2)));
+    }
+    __syncthreads();
+    r.rate = corrected[0];
+    r.low = corrected[1];
   }
   const int lane = threadIdx.x & 63;
   const int ti = tensor_of(lane < a.count, lane < a.count ? a.first[lane] : 0, blockIdx.x);
@@ -213,7 +231,6 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwArgs a) {
   const int64_t i0 = ((int64_t)(blockIdx.x - a.first[ti]) * (kThreads / 64) + wave) * kWaveElems;
   if (i0 >= n) return;
   const int64_t i = i0 + lane * kPer;
-  Rates r{a.b1, a.c1, a.b2, a.c2, a.eps, a.rate, a.low};
   float decay = (float)t.decay;
   uint32_t seed = a.seed;
   if (a.schedule) {

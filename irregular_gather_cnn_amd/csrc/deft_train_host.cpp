@@ -286,7 +286,7 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
       !(d->beta1 >= 0.0 && d->beta1 < 1.0) || !(d->beta2 >= 0.0 && d->beta2 < 1.0) || !(d->eps >= 0.0) ||
       !std::isfinite(d->lr) || !std::isfinite(d->eps) || (d->master != 0 && d->p_dtype == DEFT_F32))
     return DEFT_ERR_BAD_DESC;
-  if (!aligned4(control) || ((uintptr_t)schedule & 7u)) return DEFT_ERR_ALIGN;
+  if (!aligned4(control) || !aligned4(d->skipped) || ((uintptr_t)schedule & 7u)) return DEFT_ERR_ALIGN;
   for (int i = 0; i < count; ++i) {
     const deft_adamw_tensor& x = t[i];
     if (x.n < 0 || !(x.weight_decay >= 0.0) || !std::isfinite(x.weight_decay)) return DEFT_ERR_BAD_DESC;
@@ -310,6 +310,12 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
   a.seed = d->seed;
   a.control = control;
   a.schedule = schedule;
+  a.skipped = d->skipped;
+  a.lr = d->lr;
+  a.log1 = std::log2(d->beta1);
+  a.log2 = std::log2(d->beta2);
+  a.step = d->step;
+  a.lead = 1;
   // A step over more than the last-level cache holds leaves nothing of itself there
   // for the next one.
   double elems = 0.0;
@@ -324,7 +330,7 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
       const hipError_t e = deft::launch_adamw(a, (uint32_t)blocks, d->p_dtype, d->g_dtype, d->state_bits,
                                               d->master != 0, once, (hipStream_t)stream);
       if (e != hipSuccess) return status_of(e);
-      a.count = 0;
+      a.count = a.lead = 0;
       blocks = 0;
     }
     if (!more) continue;

@@ -112,7 +112,7 @@ class AdamW:
     a list of fp32 tensors.  ``weight_decay``: one number or one per tensor.
     ``states``: None (zeros) or a list of (m, v, m_scale, v_scale) per param,
     updated in place (the scales None with 32 bits), as :attr:`states` of an
-    earlier run whose :attr:`steps` is passed as ``step``.
+    earlier run whose :meth:`taken` steps are passed as ``step``.
 
     The addresses of all tensors are taken here and in :meth:`bind`, and that
     memory is held: a tensor that is given other memory later on (``p.data =
@@ -145,8 +145,9 @@ class AdamW:
                 raise ValueError("%d %s for %d params" % (len(got), what, len(self.params)))
         self._check_states(bits)
         self.lr, self.steps, self.seed = lr, int(step), int(seed)
+        self.skipped = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._desc = _lib.deft_adamw_desc(p_dtype, self.grads.dtype, bits, 1 if self.masters else 0, 0, lr, betas[0],
-                                          betas[1], eps, 0)
+                                          betas[1], eps, 0, self.skipped.data_ptr())
         self._list = (_lib.deft_adamw_tensor * len(self.params))()
         for k, p in enumerate(self.params):
             m, v, ms, vs = self.states[k]
@@ -189,6 +190,10 @@ class AdamW:
         """``control`` of the gradients (see :class:`GradNorm`), for :meth:`step`."""
         return self._norm(max_norm, inv_scale)
 
+    def taken(self):
+        """How many steps were taken: those counted less those skipped.  Waits for the device."""
+        return self.steps - int(self.skipped.item())
+
     def step_seed(self, step):
         """The seed that rounds the 8-bit states of step number ``step``."""
         return (self.seed + step * 0x9E3779B9) & 0xFFFFFFFF
@@ -196,9 +201,11 @@ class AdamW:
     def step(self, control=None, lr=None, schedule=None):
         """One step.  ``control``: what :meth:`grad_norm` returned; its factor
         multiplies the gradients and the step writes nothing if they are not
-        finite (it counts all the same).  ``lr``: from now on.  ``schedule``:
-        4 device doubles {lr, 1 - beta1^t, 1 - beta2^t, seed} that the kernels
-        read in place of the host's, for a step captured in a graph."""
+        finite.  :attr:`steps` counts it all the same, as the host does not
+        know; the bias corrections of later steps do not (:attr:`skipped`, on
+        the device).  ``lr``: from now on.  ``schedule``: 4 device doubles {lr,
+        1 - beta1^t, 1 - beta2^t, seed} that the kernels read in place of the
+        host's and of that count, for a step captured in a graph."""
         if lr is not None:
             self.lr = lr
         if control is not None or schedule is not None:
