@@ -371,6 +371,8 @@ int deft_norm_backward(const deft_norm_desc* d, const void* x, const void* gamma
 
 /* Elements that share one scale of an 8-bit state. */
 #define DEFT_STATE_BLOCK 256
+/* Bytes of the record of skipped steps. */
+#define DEFT_SKIPS_BYTES 48
 
 typedef struct deft_adamw_desc {
   int p_dtype, g_dtype; /* enum deft_dtype of the weights and of the gradients */
@@ -380,7 +382,8 @@ typedef struct deft_adamw_desc {
   int64_t step;         /* this step's number, from 1 */
   double lr, beta1, beta2, eps; /* lr, eps >= 0; 0 <= beta < 1 */
   uint32_t seed;        /* 8-bit states: a new one for each step */
-  uint32_t* skipped;    /* device, may be NULL: how many steps control has skipped, 0 at first */
+  uint32_t* skipped;    /* device, DEFT_SKIPS_BYTES, zeroed before the first step; may be NULL.  The first
+                           word is how many steps control has skipped; the rest is the calls' own */
 } deft_adamw_desc;
 
 typedef struct deft_adamw_tensor {
@@ -413,15 +416,16 @@ typedef struct deft_adamw_tensor {
  * multiplies the gradients; if it says that they are not finite, the step
  * writes nothing, but adds 1 to desc.skipped.
  * desc.skipped: a step's number in 1 - beta^step is desc.step less this count, so
- * skipped steps leave no mark on later ones, without a copy to the host.  Without
- * it, or with a schedule, they count as steps.
+ * skipped steps leave no mark on later ones, without a copy to the host.  Keep
+ * the betas while one record is in use.  Without it, or with a schedule, skipped
+ * steps count as steps.
  * schedule (device, may be NULL): 4 doubles {lr, 1 - beta1^step, 1 -
  * beta2^step, seed} that replace the descriptor's, read when the kernels run:
  * for a captured step whose rates change from replay to replay.
  * DEFT_ERR_DTYPE; DEFT_ERR_BAD_DESC (a negative size, a rate out of range,
  * masters for fp32 weights); DEFT_ERR_UNSUPPORTED (over 2^24 - 1 workgroups of
  * 1024 elements in one tensor); DEFT_ERR_NULLPTR; DEFT_ERR_ALIGN (tensors 16
- * bytes, scales, control and skipped 4, schedule 8).  Checks run before any launch. */
+ * bytes, scales and control 4, schedule and skipped 8).  Checks run before any launch. */
 int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int count, const float* control,
                     const double* schedule, void* stream);
 

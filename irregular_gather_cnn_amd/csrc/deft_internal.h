@@ -155,10 +155,22 @@ struct AdamwArgs {
   uint32_t seed;
   const float* control;    // nullable
   const double* schedule;  // nullable
-  uint32_t* skipped;       // nullable; where it is above 0, rate and low are computed from:
-  double lr, log1, log2;   // log2 of beta1 and beta2
+  struct AdamwSkips* skips;  // nullable; where steps were skipped, rate and low are made from it and from:
+  double lr, log1, log2;     // log2 of beta1 and beta2
   int64_t step;
 };
+// The device's record of skipped steps.  Corrections take fp64 powers, which every thread's
+// computing them made a third of a large step's operations (284 us against 255 of 77 M
+// elements): one thread of each call computes the next call's, where the count is not 0.
+struct AdamwSkips {
+  uint32_t count, unused[3];
+  struct Next {
+    double inverse;  // 1 / (1 - beta1^taken)
+    float low;       // 1 / sqrt(1 - beta2^taken)
+    uint32_t taken;  // the number of the step that they are for, among those taken
+  } next[2];         // of steps of even and of odd number: a call reads one and writes the other
+};
+static_assert(sizeof(AdamwSkips) == DEFT_SKIPS_BYTES, "include/deft.h");
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
 hipError_t launch_adamw(const AdamwArgs& a, uint32_t blocks, int p_dtype, int g_dtype, int bits, bool master,
                         bool once, hipStream_t st);

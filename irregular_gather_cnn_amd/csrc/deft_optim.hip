@@ -189,6 +189,22 @@ __device__ __forceinline__ void adamw(float g, float& m, float& v, float& root, 
   p = p * decay - (m / (root * r.low + r.eps)) * r.rate;
 }
 
+// Where steps were skipped: the number of a call's step among those taken, the
+// corrections of such a step, and those of the next call, by one thread.
+__device__ __forceinline__ uint32_t taken_by(int64_t step, uint32_t skipped) {
+  return step > skipped ? (uint32_t)(step - skipped) : 1;
+}
+__device__ __forceinline__ AdamwSkips::Next correction(const AdamwArgs& a, uint32_t taken) {
+  AdamwSkips::Next r;
+  r.inverse = 1.0 / (1.0 - exp2((double)taken * a.log1));
+  r.low = (float)(1.0 / sqrt(1.0 - exp2((double)taken * a.log2)));
+  r.taken = taken;
+  return r;
+}
+__device__ __forceinline__ void correct_next(const AdamwArgs& a, uint32_t skipped) {
+  a.skips->next[(a.step + 1) & 1] = correction(a, taken_by(a.step + 1, skipped));
+}
+
 }  // namespace
 
 // P: weights' type, G: gradients', BITS: states', MASTER: fp32 masters beside bf16 weights.
@@ -200,28 +216,26 @@ __device__ __forceinline__ void adamw(float g, float& m, float& v, float& root, 
 template <typename P, typename G, int BITS, bool MASTER, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwArgs a) {
 #pragma clang fp contract(off)
-  const uint32_t skipped = a.skipped ? *a.skipped : 0;
-  float coef = 1.f;
-  if (a.control) {
+  AdamwSkips* const skips = a.skips;
+  float coef = 1.f, finite = 1.f;
+  uint32_t skipped = 0;
+  if (a.control && skips) {  // one wait for both
     coef = a.control[1];
-    if (a.control[2] == 0.f) {  // gradients not finite: the step is counted, and nothing else is written
-      if (a.skipped && a.lead && blockIdx.x == 0 && threadIdx.x == 0) *a.skipped = skipped + 1;
-      return;
-    }
+    finite = a.control[2];
+    skipped = skips->count;
+  } else if (a.control) {
+    coef = a.control[1];
+    finite = a.control[2];
+  } else if (skips) {
+    skipped = skips->count;
   }
-  Rates r{a.b1, a.c1, a.b2, a.c2, a.eps, a.rate, a.low};
-  if (skipped && !a.schedule) {
-    // The corrections of the steps that were taken.  A wave's work for the workgroup: in every wave, these
-    // fp64 operations would take as long as a third of the step's memory accesses.
-    __shared__ float corrected[2];
-    if (threadIdx.x < 64) {
-      const double taken = (double)(a.step > skipped ? a.step - skipped : 1);
-      corrected[0] = (float)(a.lr / (1.0 - exp2(taken * a.log1)));
-      corrected[1] = (float)(1.0 / sqrt(1.0 - exp2(taken * a.log2)));
+  const bool lead = a.lead && blockIdx.x == 0 && threadIdx.x == 0;
+  if (finite == 0.f) {  // the step is counted, and nothing else is written
+    if (skips && lead) {
+      skips->count = skipped + 1;
+      correct_next(a, skipped + 1);
     }
-    __syncthreads();
-    r.rate = corrected[0];
-    r.low = corrected[1];
+    return;
   }
   const int lane = threadIdx.x & 63;
   const int ti = tensor_of(lane < a.count, lane < a.count ? a.first[lane] : 0, blockIdx.x);
@@ -231,6 +245,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwArgs a) {
   const int64_t i0 = ((int64_t)(blockIdx.x - a.first[ti]) * (kThreads / 64) + wave) * kWaveElems;
   if (i0 >= n) return;
   const int64_t i = i0 + lane * kPer;
+  Rates r{a.b1, a.c1, a.b2, a.c2, a.eps, a.rate, a.low};
   float decay = (float)t.decay;
   uint32_t seed = a.seed;
   if (a.schedule) {
@@ -239,6 +254,13 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwArgs a) {
     r.low = (float)(1.0 / sqrt(a.schedule[2]));
     decay = (float)(1.0 - lr * t.decay);
     seed = (uint32_t)(int64_t)a.schedule[3];
+  } else if (skipped) {
+    AdamwSkips::Next now = skips->next[a.step & 1];
+    // not what the last call left where it was captured, and is replayed with one number
+    if (now.taken != taken_by(a.step, skipped)) now = correction(a, taken_by(a.step, skipped));
+    r.rate = (float)(a.lr * now.inverse);
+    r.low = now.low;
+    if (lead) correct_next(a, skipped);
   }
   float g[4], p[4], m[4], v[4], root[4];
   load4<ONCE>((const G*)t.g, i, n, g);

@@ -15,6 +15,7 @@
 namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool dtype_ok(int t) { return t == DEFT_F32 || t == DEFT_BF16; }
 int status_of(hipError_t e) { return e == hipSuccess ? DEFT_OK : deft::report_hip_error(e); }
@@ -286,7 +287,7 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
       !(d->beta1 >= 0.0 && d->beta1 < 1.0) || !(d->beta2 >= 0.0 && d->beta2 < 1.0) || !(d->eps >= 0.0) ||
       !std::isfinite(d->lr) || !std::isfinite(d->eps) || (d->master != 0 && d->p_dtype == DEFT_F32))
     return DEFT_ERR_BAD_DESC;
-  if (!aligned4(control) || !aligned4(d->skipped) || ((uintptr_t)schedule & 7u)) return DEFT_ERR_ALIGN;
+  if (!aligned4(control) || !aligned8(d->skipped) || !aligned8(schedule)) return DEFT_ERR_ALIGN;
   for (int i = 0; i < count; ++i) {
     const deft_adamw_tensor& x = t[i];
     if (x.n < 0 || !(x.weight_decay >= 0.0) || !std::isfinite(x.weight_decay)) return DEFT_ERR_BAD_DESC;
@@ -310,7 +311,7 @@ int deft_adamw_step(const deft_adamw_desc* d, const deft_adamw_tensor* t, int co
   a.seed = d->seed;
   a.control = control;
   a.schedule = schedule;
-  a.skipped = d->skipped;
+  a.skips = (deft::AdamwSkips*)d->skipped;
   a.lr = d->lr;
   a.log1 = std::log2(d->beta1);
   a.log2 = std::log2(d->beta2);

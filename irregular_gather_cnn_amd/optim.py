@@ -145,9 +145,10 @@ class AdamW:
                 raise ValueError("%d %s for %d params" % (len(got), what, len(self.params)))
         self._check_states(bits)
         self.lr, self.steps, self.seed = lr, int(step), int(seed)
-        self.skipped = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._skips = torch.zeros(_lib.DEFT_SKIPS_BYTES // 4, dtype=torch.int32, device=self.device)
+        self.skipped = self._skips[:1]
         self._desc = _lib.deft_adamw_desc(p_dtype, self.grads.dtype, bits, 1 if self.masters else 0, 0, lr, betas[0],
-                                          betas[1], eps, 0, self.skipped.data_ptr())
+                                          betas[1], eps, 0, self._skips.data_ptr())
         self._list = (_lib.deft_adamw_tensor * len(self.params))()
         for k, p in enumerate(self.params):
             m, v, ms, vs = self.states[k]

@@ -125,3 +125,22 @@ def test_a_captured_step_counts_its_skips_on_the_device():
         assert opt.skipped.item() == k + 1
         for a, b in zip(opt.params + [t for t in opt.states[0] if t is not None], before):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_what_a_call_leaves_for_the_next_one_is_what_that_would_compute():
+    """The corrections that the last call left, and those computed where it left none: the same bits."""
+    a, ga, _ = make([3000, 40], "bf16", "bf16", 8, True, 25)
+    b, gb, _ = make([3000, 40], "bf16", "bf16", 8, True, 25)
+    for k in range(8):
+        for opt, g in ((a, ga), (b, gb)):
+            if opt is b:
+                opt._skips[4:].zero_()
+            if k in (1, 2, 5):
+                skip(opt, g)
+            else:
+                opt.step(control=opt.grad_norm())
+        for x, y in zip(a.params + a.masters + [t for s in a.states for t in s],
+                        b.params + b.masters + [t for s in b.states for t in s]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert a.taken() == b.taken() == 5
