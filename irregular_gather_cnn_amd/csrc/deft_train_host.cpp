@@ -65,8 +65,8 @@ struct NormCut {
 // kernels take up to 128 registers, the backward's up to 256.
 int resident(const NormCut& r, bool back, int threads) { return r.cus * (back ? 512 : 1024) / threads; }
 
-// One slice for a group (or a band of groups), where it fits the registers:
-// 32 accesses a thread forward, 16 of x and of dy backward.  It needs no
+// One slice for a group (or a band of groups), where it fits the registers: 32
+// accesses a thread forward, 16 of x and of dy backward.  It needs no
 // exchange, which costs 3 to 5 us, but only as many compute units work as there
 // are groups; so where these leave units idle, it pays up to about 5 us of one
 // unit's work, counted in vector operations an element, of which reading and
@@ -74,8 +74,21 @@ int resident(const NormCut& r, bool back, int threads) { return r.cus * (back ? 
 // (us in one slice and joined): 12 bands of 9000 elements, gelu fp32, 8.6 and 10.7;
 // 5 groups of 20252, relu bf16, 6.1 and 7.1; 10 of 43590, none bf16, 10.2 and 8.6; 50
 // of 42476, none fp32, 18.7 and 10.9.
+//
+// 17 to 32 accesses forward fill a unit with one workgroup (and 7 to 24 registers
+// of a thread spill, but for fp32 channels last, which takes 177).  That pays
+// where all run at once: against slices, 240 groups channels first fp32 23.5 us
+// and 24.4, 240 bands channels last bf16 30.9 and 33.1, 231 groups channels first
+// bf16 23.9 and 33.1.  A second round that is not full loses it: 309 groups
+// channels first fp32 37 and 28, 574 66 and 43, 1024 100 and 84; channels last bf16
+// 8x640x7000 69 and 47.  Channels first in bf16 gains over full rounds: 512 groups
+// 48 and 52, 670 60 and 77, but 578 67 and 57, 308 48 and 39.
 bool whole_pays(const deft_norm_desc& d, const NormCut& r, bool back, int V, int rounds, int64_t units, int64_t elems) {
   if (rounds > (V == 1 || back ? 16 : 32)) return false;
+  if (rounds > 16 && units > r.cus) {
+    const int64_t room = (units + r.cus - 1) / r.cus * r.cus;
+    if (d.layout != DEFT_CHANNELS_FIRST || d.dtype != DEFT_BF16 || units * 5 < room * 4) return false;
+  }
   if (units >= r.cus * 3 / 4) return true;
   const int act = d.act == DEFT_ACT_GELU ? 40 : d.act == DEFT_ACT_SILU ? 24 : 12;
   const int bytes = d.dtype == DEFT_F32 ? 52 : 26;

@@ -52,3 +52,15 @@ def test_refusals():
         assert e.value.code == code
     with pytest.raises(L.DeftError):
         L.deft_debug_norm_cut(desc(2, 64, 500, 2, "channels_first"), False, -1)
+
+
+@pytest.mark.parametrize("layout,dtype,n,c,s,g,form", [
+    # one workgroup a unit: all 256 at once, or a second round
+    ("channels_first", "f32", 10, 96, 10688, 24, WHOLE), ("channels_first", "f32", 3, 412, 9992, 103, JOINT),
+    ("channels_first", "f32", 32, 512, 2500, 32, JOINT), ("channels_last", "bf16", 40, 132, 3138, 6, WHOLE),
+    ("channels_last", "bf16", 8, 640, 7000, 40, TWICE), ("channels_last", "f32", 12, 210, 1725, 35, WHOLE),
+    # bf16 channels first: rounds that are 4/5 full
+    ("channels_first", "bf16", 10, 335, 16678, 67, WHOLE), ("channels_first", "bf16", 4, 308, 31434, 77, JOINT),
+    ("channels_first", "bf16", 34, 221, 4345, 17, JOINT)])
+def test_forward_groups_that_fill_a_unit_run_in_full_rounds(layout, dtype, n, c, s, g, form):
+    assert L.deft_debug_norm_cut(desc(n, c, s, g, layout, dtype), False, 256)["form"] == form
