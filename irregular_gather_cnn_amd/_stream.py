@@ -1,4 +1,4 @@
-"""The device's current stream as the integer handle that the C ABI takes."""
+"""A device's current stream as the integer handle that the C ABI takes."""
 from __future__ import annotations
 
 import torch
@@ -9,10 +9,11 @@ _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def current_stream(device: torch.device) -> int:
-    if _raw is not None and device.index is not None:
-        return _raw(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+def current_stream(index: int) -> int:
+    """That of GPU `index`, a tensor's ``get_device()``."""
+    if index < 0:
+        raise ValueError("the tensors are not on a GPU")
+    return _raw(index) if _raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def elsewhere(index: int) -> bool:

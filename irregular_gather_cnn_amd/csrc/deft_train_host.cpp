@@ -490,7 +490,8 @@ int deft_norm_backward(const deft_norm_desc* d, const void* x, const void* gamma
   if (d->n == 0 || d->s == 0)
     return params ? status_of(deft::launch_norm_params(nullptr, 0, d->c, dgamma, dbeta, d->dtype, s)) : DEFT_OK;
   NormCut f, r;
-  if ((st = norm_cut(*d, false, f)) != DEFT_OK || (st = norm_cut(*d, true, r)) != DEFT_OK) return st;
+  const int cus = deft::compute_units();
+  if ((st = norm_cut(*d, false, f, cus)) != DEFT_OK || (st = norm_cut(*d, true, r, cus)) != DEFT_OK) return st;
   if (!x || !gamma || !beta || !mean || !rstd || !dy) return DEFT_ERR_NULLPTR;
   if (!aligned16(x) || !aligned16(gamma) || !aligned16(beta) || !aligned16(mean) || !aligned16(rstd) ||
       !aligned16(dy))

@@ -89,7 +89,7 @@ class GroupNormAct:
             with torch.cuda.device(self._index):
                 return self.forward(x, gamma, beta, y, mean, rstd)
         code = self._forward(self._ref, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(), mean.data_ptr(),
-                             rstd.data_ptr(), self._ws, self.ws_bytes, current_stream(self.device))
+                             rstd.data_ptr(), self._ws, self.ws_bytes, current_stream(self._index))
         if code:
             raise _lib.DeftError(code, "deft_norm_forward")
         return y, mean, rstd
@@ -104,18 +104,23 @@ class GroupNormAct:
                 or unfit(dy, self._image) or unfit(mean, self._stat) or unfit(rstd, self._stat)):
             self._refuse(x=x, gamma=gamma, beta=beta, mean=mean, rstd=rstd, dy=dy)
         if out is None:
-            out = dict(dx=torch.empty_like(x), dgamma=torch.empty_like(gamma), dbeta=torch.empty_like(beta))
+            dx, dgamma, dbeta = torch.empty_like(x), torch.empty_like(gamma), torch.empty_like(beta)
+            out = dict(dx=dx, dgamma=dgamma, dbeta=dbeta)
         else:
             if not out.keys() <= _GRADIENTS:
                 raise ValueError("out may hold %s, got %s" % (sorted(_GRADIENTS), sorted(out)))
-            self._refuse(**out)
+            dx, dgamma, dbeta = out.get("dx"), out.get("dgamma"), out.get("dbeta")
+            if (dx is not None and unfit(dx, self._image) or dgamma is not None and unfit(dgamma, self._channel)
+                    or dbeta is not None and unfit(dbeta, self._channel)):
+                self._refuse(**out)
         if elsewhere(self._index):
             with torch.cuda.device(self._index):
                 return self.backward(x, gamma, beta, mean, rstd, dy, out)
-        dx, dgamma, dbeta = (None if out.get(k) is None else out[k].data_ptr() for k in ("dx", "dgamma", "dbeta"))
         code = self._backward(self._ref, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), mean.data_ptr(),
-                              rstd.data_ptr(), dy.data_ptr(), dx, dgamma, dbeta, self._ws, self.ws_bytes,
-                              current_stream(self.device))
+                              rstd.data_ptr(), dy.data_ptr(), None if dx is None else dx.data_ptr(),
+                              None if dgamma is None else dgamma.data_ptr(),
+                              None if dbeta is None else dbeta.data_ptr(), self._ws, self.ws_bytes,
+                              current_stream(self._index))
         if code:
             raise _lib.DeftError(code, "deft_norm_backward")
         return out

@@ -95,7 +95,7 @@ class GradNorm:
             with torch.cuda.device(g.index):
                 return self(max_norm, inv_scale)
         code = self._call(g.pointers, self._n, len(g.sizes), g.dtype, max_norm, inv_scale, self._out, self._ws,
-                          self.ws_bytes, current_stream(g.device))
+                          self.ws_bytes, current_stream(g.index))
         if code:
             raise _lib.DeftError(code, "deft_grad_norm")
         return self.control
@@ -220,7 +220,7 @@ class AdamW:
         d = self._desc
         d.lr, d.step, d.seed = self.lr, self.steps + 1, self.step_seed(self.steps + 1)
         code = self._call(self._ref, self._list, len(self.params), None if control is None else control.data_ptr(),
-                          None if schedule is None else schedule.data_ptr(), current_stream(self.device))
+                          None if schedule is None else schedule.data_ptr(), current_stream(self.grads.index))
         if code:
             raise _lib.DeftError(code, "deft_adamw_step")
         self.steps += 1
