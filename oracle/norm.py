@@ -4,9 +4,12 @@ Only ``tests/`` may import this module; the product path never does.
 
 The formulas of include/deft.h (deft_norm_forward, deft_norm_backward) in
 float64 on channels-first arrays [n][c][s], with bounds on what fp32 sums and
-roundings may add to them: ``K`` counts the longest chain of additions a value
-passes through (a thread's 16 accesses of 8 elements, a segment's 64 steps in
-LDS, the combination of the slices).
+roundings may add to them.  Forward, a thread sums up to 32 accesses in fp32
+(``CHAIN``: an addition each, two in bf16, which may cut off where others round,
+and 8 more that join its columns); beyond it all sums are fp64, and each slice's
+mean is rounded once.  Backward, ``K`` counts the longest chain of fp32 additions
+that a value passes through: 64 rows or 128 elements of a thread, at most 22 that
+join threads, 16 waves, then slices or images in shares of 64 with 20 to join them.
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ from scipy.special import ndtr
 
 H = 2.0 ** -24
 K = 256
+CHAIN = {"f32": 40, "bf16": 136}
 
 
 def act(name, z):
@@ -64,9 +68,13 @@ def forward(x, gamma, beta, g, eps, name, dtype):
     m2 = (d * d).sum(2)
     var = m2 / m
     rstd = 1 / np.sqrt(var + eps)
-    e_mean = K * H * np.abs(xg).mean(2) + H * np.abs(mean)
+    size, std = np.abs(xg).mean(2), np.sqrt(var)
+    e_mean = (CHAIN[dtype] + 2) * H * size + H * np.abs(mean)
     # d is rounded and off by the mean's error: the sum of d is zero, so that counts squared
-    e_var = (K + 8) * H * var + (e_mean + 2 * H * np.abs(xg).mean(2)) ** 2 * 2
+    e_var = (K + 8) * H * var + (K * H * size + H * np.abs(mean) + 2 * H * size) ** 2 * 2
+    if dtype == "f32":
+        # or: squares about each thread's own mean, which then counts by its distance from the group's
+        e_var = np.minimum(e_var, 140 * H * var + 2 * std * (CHAIN[dtype] + 1) * H * np.abs(xg).max(2) + e_mean ** 2)
     r_rstd = 0.5 * e_var / (var + eps) + 4 * H
     mu, rs = _per_channel(mean, n, c), _per_channel(rstd, n, c)
     em, rr = _per_channel(e_mean, n, c), _per_channel(r_rstd, n, c)
