@@ -50,7 +50,7 @@ def test_handles_hold_the_memory_they_point_to(bits):
     for t in p + g + opt.masters + [t for s in opt.states for t in s if t is not None]:
         t.data = torch.empty_like(t)
     gc.collect()
-    kept = {t.data_ptr() for t in gc.get_objects() if type(t) is torch.Tensor}
+    kept = {t.data_ptr() for t in opt._held + opt.grads.held + norm.grads.held}
     for item in opt._list:
         for field in ("p", "g", "m", "v", "master") + (("m_scale", "v_scale") if bits == 8 else ()):
             assert getattr(item, field) in kept, field
