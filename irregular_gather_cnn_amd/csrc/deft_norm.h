@@ -102,8 +102,8 @@ __device__ __forceinline__ void apart() { __builtin_amdgcn_sched_barrier(0); }
 // approximations are enough: the product's rounding costs x 2^-24 of the result.
 // fp32 silu takes that rounding back, and one Newton step (the error of its sums
 // falls from 2.2e-7 to 1e-7 for two operations in ten more).
-// gelu takes the plain exponential in fp32, too: it stands in the tail alone, where
-// its (z^2 + 2) 2^-24 is beside the tail's own 6e-7.
+// gelu takes the plain exponential in fp32, too: it scales the tail, whose error it
+// makes (z^2 + 2) 2^-24 of itself; for z > 0 that is at most 2^-23 of y.
 template <typename T> __device__ __forceinline__ float exp_of(float x) {
   const float t = x * 1.44269504f, e = __builtin_amdgcn_exp2f(t);
   if (sizeof(T) == 2) return e;

@@ -4,10 +4,10 @@
 // registers, so x is read once.  Statistics must not lose the variance where the
 // mean is far from zero: all sums beyond a thread's are fp64.  Within a thread,
 // fp32 elements give the squares about the mean of its own ones.  bf16 elements
-// give plain sums of themselves and of their squares, at most 256 of each.  Products of bf16 numbers are exact in fp32, and so are
-// those sums where the numbers are near to each other, which is where the
-// difference of the two needs it; this takes one instruction an element
-// (v_dot2c_f32_bf16) in place of five.
+// give plain sums of themselves and of their squares, at most 256 of each.
+// Products of bf16 numbers are exact in fp32, and so are those sums where the
+// numbers are near to each other, which is where the difference of the two needs
+// it; this takes one instruction an element (v_dot2c_f32_bf16) in place of five.
 #include "deft_norm.h"
 
 namespace deft {
@@ -55,7 +55,7 @@ __device__ __forceinline__ bool combine_joint(const NormArgs& a, int layout, con
 // ones in the order ((n, b), k) over all XCDs, so that a cluster starts together.
 // Bound by memory from a few million elements on: 32x1024x512 fp32 takes 23 us (5.8
 // TB/s), 2x65536x320 bf16 53 (read twice: 4.7 TB/s the first time, then 5.7); by
-// vector operations with gelu in bf16 (27 an element; 16x784x512 15 us against 11);
+// vector operations with gelu in bf16 (28 an element; 16x784x512 15 us against 11);
 // by latency below: load, reduction and store take 5 us, an exchange 3 to 5 more.
 // part: [n][g][slices]{mean, M2}.
 template <typename T, int V, int U, int MODE>

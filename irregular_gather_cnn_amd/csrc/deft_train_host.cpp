@@ -81,7 +81,7 @@ int resident(const NormCut& r, bool back, int threads) { return r.cus * (back ? 
 // and 24.4, 240 bands channels last bf16 30.9 and 33.1, 231 groups channels first
 // bf16 23.9 and 33.1.  A second round that is not full loses it: 309 groups
 // channels first fp32 37 and 28, 574 66 and 43, 1024 100 and 84; channels last bf16
-// 8x640x7000 69 and 47.  Channels first in bf16 gains over full rounds: 512 groups
+// 8 images of 7000 x 640 69 and 47.  Channels first in bf16 gains over full rounds: 512 groups
 // 48 and 52, 670 60 and 77, but 578 67 and 57, 308 48 and 39.
 bool whole_pays(const deft_norm_desc& d, const NormCut& r, bool back, int V, int rounds, int64_t units, int64_t elems) {
   if (rounds > (V == 1 || back ? 16 : 32)) return false;
