@@ -447,6 +447,66 @@ int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtyp
  * count themselves in it. */
 size_t deft_grad_norm_workspace_bytes(int count);
 
+/* ---- Pointwise (1x1) convolution in 8 bits, with its gradients ----
+ *
+ * x is [n][c_in][s] (DEFT_CHANNELS_FIRST) or [n][s][c_in] (DEFT_CHANNELS_LAST),
+ * y and dy likewise with c_out; w is [c_out][c_in].  Over the rows r, the n * s
+ * positions in their order,
+ *   y[r][o]  = sum_k qx[r][k] qw[o][k] + b[o]
+ *   dx[r][k] = sum_o qdy[r][o] qw[o][k]
+ *   dw[o][k] = sum_r q'dy[r][o] q'x[r][k],   db[o] = sum_r dy[r][o]
+ * where q stands for values of e4m3 (OCP, 448 its largest) times a power of two
+ * that a block of values shares: qx and qdy in blocks of 128 consecutive channels
+ * of a row, q'x and q'dy in blocks of 128 consecutive rows of a channel, qw in
+ * blocks of 128 x 128 (all from the first channel or row on; the last blocks may
+ * be smaller).  With most the largest magnitude of a block's finite values, its
+ * power is 2^e with the least whole e >= -127 for which most <= 448 * 2^e, and
+ * each value is rounded to the nearest multiple, ties to even.  A NaN or an
+ * infinity makes NaN of the sums that it enters, and of no others.  Products are
+ * exact, sums fp32, results rounded once; calls repeat their bits.  bf16: within
+ * each 8 consecutive terms, what lies under 2^-13 of the largest is cut off before
+ * they are added (the 8-bit matrix instructions' sum), 1.5e-5 of a result. */
+#define DEFT_PW8_BLOCK 128
+
+typedef struct deft_pw8_desc {
+  int n, s;              /* images, positions (h * w, or steps) */
+  int c_in, c_out;
+  int layout;            /* enum deft_layout of x, y, dx and dy */
+  int dtype;             /* enum deft_dtype of all tensors */
+  int training;          /* 1: packed weights and forward are for deft_pw8_backward, too */
+} deft_pw8_desc;
+
+/* DEFT_OK, or the code with which the calls below refuse the descriptor:
+ * DEFT_ERR_BAD_DESC (negative n or s, c_in or c_out < 1, layout or training out
+ * of range), DEFT_ERR_DTYPE, DEFT_ERR_UNSUPPORTED (over 2^31 - 129 rows or 2^20
+ * channels; launches of 2^32 threads).  The sizes below are 0 for it, then. */
+int deft_pw8_desc_validate(const deft_pw8_desc* d);
+
+/* Bytes of the packed weights, and of what a training forward saves. */
+size_t deft_pw8_packed_bytes(const deft_pw8_desc* d);
+size_t deft_pw8_saved_bytes(const deft_pw8_desc* d);
+/* Bytes of a workspace for the calls below on this descriptor; it depends on the
+ * current device's number of units.  Nothing is kept in it from call to call. */
+size_t deft_pw8_workspace_bytes(const deft_pw8_desc* d);
+
+/* Codes of w, once for all calls until it changes.  Every byte of `packed` that
+ * the other calls read is written.  It serves every n, s and layout. */
+int deft_pw8_pack(const deft_pw8_desc* d, const void* w, void* packed, void* stream);
+
+/* y; bias may be NULL.  training: writes `saved`, what the backward needs of x.
+ * n * s = 0 is a no-op.  y must not overlap x.  Errors of all calls, besides the
+ * descriptor's: DEFT_ERR_NULLPTR, DEFT_ERR_ALIGN (pointers 16 bytes),
+ * DEFT_ERR_WORKSPACE, DEFT_ERR_BAD_DESC (an overlap; a backward without
+ * training); checks run before any launch. */
+int deft_pw8_forward(const deft_pw8_desc* d, const void* x, const void* packed, const void* bias, void* y, void* saved,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients at dy, with `saved` as the forward left it and the packed weights
+ * that it used; any of dx, dw and db may be NULL and is not computed then.  n * s
+ * = 0 writes zeros to dw and db.  dx must not overlap dy. */
+int deft_pw8_backward(const deft_pw8_desc* d, const void* saved, const void* packed, const void* dy, void* dx, void* dw,
+                      void* db, void* workspace, size_t ws_bytes, void* stream);
+
 /* Per-kernel timing for benchmarks (host-side events only; no device memory).
  * deft_timing_start(capacity) creates `capacity` event pairs for the calling
  * thread; while active, each kernel that deft_forward / deft_backward /

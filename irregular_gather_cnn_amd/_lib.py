@@ -33,7 +33,9 @@ EXPORTED = ["deft_desc_validate", "deft_plan_create", "deft_plan_create_forced",
             "deft_timing_get", "deft_dwconv1d_forward", "deft_dwpw1d_forward",
             "deft_adamw_step", "deft_grad_norm", "deft_grad_norm_workspace_bytes",
             "deft_norm_desc_validate", "deft_norm_workspace_bytes", "deft_norm_forward",
-            "deft_norm_backward", "deft_debug_norm_patience", "deft_debug_norm_cut"]
+            "deft_norm_backward", "deft_debug_norm_patience", "deft_debug_norm_cut",
+            "deft_pw8_desc_validate", "deft_pw8_packed_bytes", "deft_pw8_saved_bytes", "deft_pw8_workspace_bytes",
+            "deft_pw8_pack", "deft_pw8_forward", "deft_pw8_backward"]
 LAYOUTS = {"channels_first": 0, "channels_last": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
@@ -81,6 +83,10 @@ class deft_norm_desc(ctypes.Structure):
         ("eps", ctypes.c_double)]
 
 
+class deft_pw8_desc(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int) for k in ("n", "s", "c_in", "c_out", "layout", "dtype", "training")]
+
+
 _lib = None
 
 
@@ -122,6 +128,13 @@ def load() -> ctypes.CDLL:
         "deft_debug_norm_patience": (None, [ctypes.c_uint32]),
         "deft_norm_forward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 7 + [sz, vp]),
         "deft_norm_backward": (i, [ctypes.POINTER(deft_norm_desc)] + [vp] * 10 + [sz, vp]),
+        "deft_pw8_desc_validate": (i, [ctypes.POINTER(deft_pw8_desc)]),
+        "deft_pw8_packed_bytes": (sz, [ctypes.POINTER(deft_pw8_desc)]),
+        "deft_pw8_saved_bytes": (sz, [ctypes.POINTER(deft_pw8_desc)]),
+        "deft_pw8_workspace_bytes": (sz, [ctypes.POINTER(deft_pw8_desc)]),
+        "deft_pw8_pack": (i, [ctypes.POINTER(deft_pw8_desc), vp, vp, vp]),
+        "deft_pw8_forward": (i, [ctypes.POINTER(deft_pw8_desc)] + [vp] * 6 + [sz, vp]),
+        "deft_pw8_backward": (i, [ctypes.POINTER(deft_pw8_desc)] + [vp] * 7 + [sz, vp]),
         "deft_error_string": (ctypes.c_char_p, [i]),
         "deft_last_hip_error": (ctypes.c_char_p, []),
         "deft_timing_start": (i, [i]),
@@ -283,6 +296,22 @@ def deft_debug_norm_cut(desc: deft_norm_desc, back: bool, cus: int = 0) -> dict:
 
 def deft_debug_norm_patience(ticks: int) -> None:
     load().deft_debug_norm_patience(int(ticks))
+
+
+def deft_pw8_desc_validate(desc: deft_pw8_desc) -> None:
+    _check(load().deft_pw8_desc_validate(ctypes.byref(desc)), "deft_pw8_desc_validate")
+
+
+def deft_pw8_packed_bytes(desc: deft_pw8_desc) -> int:
+    return int(load().deft_pw8_packed_bytes(ctypes.byref(desc)))
+
+
+def deft_pw8_saved_bytes(desc: deft_pw8_desc) -> int:
+    return int(load().deft_pw8_saved_bytes(ctypes.byref(desc)))
+
+
+def deft_pw8_workspace_bytes(desc: deft_pw8_desc) -> int:
+    return int(load().deft_pw8_workspace_bytes(ctypes.byref(desc)))
 
 
 def deft_error_string(code: int) -> str:

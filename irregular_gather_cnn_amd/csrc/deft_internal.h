@@ -242,4 +242,57 @@ hipError_t launch_norm_bwd_sums(const NormArgs& a, int layout, int dtype, hipStr
 hipError_t launch_norm_params(const float* part, int rows, int c, void* dgamma, void* dbeta, int dtype,
                               hipStream_t st);
 
+// Pointwise convolution in 8 bits (deft_pw8_quantise.hip, deft_pw8_gemm.hip,
+// deft_pw8_few.hip).  A matrix of codes over `rows` and a depth, stored by blocks
+// of 128 of the depth: codes [blocks][rows][128], scales [blocks][pw8_scale_rows].
+constexpr int kPw8Block = 128;
+__host__ __device__ inline int64_t pw8_scale_rows(int64_t rows) { return (rows + 15) & ~(int64_t)15; }
+struct Pw8Matrix {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows;
+};
+struct Pw8QuantiseArgs {
+  const void* src;        // [lines][near], or channels first [images][lines][positions]
+  int64_t lines, near;    // near: values along memory, over all images
+  int64_t pitch;          // from line to line
+  int64_t positions;      // of an image, channels first; else 0
+  uint32_t tiles_near;
+  uint8_t* near_codes;    // nullable: rows are lines, the depth is near
+  uint8_t* near_scales;
+  uint8_t* far_codes;     // nullable: rows are near, the depth is lines
+  uint8_t* far_scales;
+  float* sums;            // nullable: [tiles of the rows][channels] sums over a tile's rows
+};
+hipError_t launch_pw8_quantise(const Pw8QuantiseArgs& a, uint32_t blocks, int dtype, bool tile, hipStream_t st);
+hipError_t launch_pw8_bias(const float* sums, int64_t tiles, int c, void* db, int dtype, hipStream_t st);
+hipError_t launch_pw8_zero(void* p, size_t bytes, hipStream_t st);
+struct Pw8Out {
+  void* p;
+  const void* bias;       // nullable: per column; with positions per row
+  int64_t rows, cols;
+  int64_t positions;      // channels first: columns are the positions of all images; else 0
+};
+struct Pw8GemmArgs {
+  Pw8Matrix a, b;         // out[i][j] = sum over the depth of a[i] b[j]
+  Pw8Out out;
+  float* part;            // nullable: [splits][rows][part_cols], joined by a second launch
+  int part_cols;
+  int blocks;             // of the depth
+  int splits, per_split;  // blocks of a split
+  int tiles_m, tiles_n;
+};
+hipError_t launch_pw8_gemm(const Pw8GemmArgs& g, int bm, int bn, int dtype, hipStream_t st);
+// Up to kPw8Few rows: x is quantised where it is used.
+constexpr int kPw8Few = 16;
+struct Pw8FewArgs {
+  const void* x;
+  Pw8Matrix w;
+  const void* bias;       // nullable
+  void* y;
+  int rows, c_in;
+  int positions;          // channels first: of an image; else 0
+};
+hipError_t launch_pw8_few(const Pw8FewArgs& a, int dtype, int cus, hipStream_t st);
+
 }  // namespace deft

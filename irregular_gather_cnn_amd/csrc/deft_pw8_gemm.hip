@@ -1,0 +1,396 @@
+// Products of 8-bit block-scaled matrices (gfx950): the pointwise convolution
+// and its gradients.
+//
+// C[i][j] = sum_k A[i][k] B[j][k] over two matrices of e4m3 codes stored by
+// blocks of 128 of k (deft_pw8_quantise.hip), each row of a block with a power
+// of two.  v_mfma_scale_f32_32x32x64 multiplies 64 codes of 32 rows by 64 of 32
+// others, with their powers of two, into fp32: twice the rate of bf16, and no
+// vector operations for the scales.  Products for fp32 results are 16-bit ones
+// (deft_pw8.h says why).
+#include <algorithm>
+
+#include "deft_device.h"
+#include "deft_internal.h"
+#include "deft_pw8.h"
+
+namespace deft {
+
+namespace {
+
+constexpr int kHalf = 64;  // bytes of a row in a stage: half of a block
+
+// Bytes straight into LDS, 4 per lane.
+__device__ __forceinline__ void load_lds4(const rsrc_t r, uint32_t lds_addr, int voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(voff), "s"(r)
+               : "memory");
+}
+
+// A number that all lanes have, computed in vector registers (quotients, 64-bit
+// minima), for the scalar resources.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
+}
+
+// The pause: a load may read a scalar register that a vector instruction wrote
+// only five states later, and the compiler does not see the loads in the assembly.
+__device__ __forceinline__ rsrc_t uniform_rsrc(uint64_t p, uint32_t bytes) {
+  rsrc_t r;
+  r.x = (int)uniform((uint32_t)p);
+  r.y = (int)uniform((uint32_t)(p >> 32));
+  r.z = (int)uniform(bytes);
+  r.w = 0x00020000;
+  asm volatile("s_nop 4" : "+s"(r));
+  return r;
+}
+
+// 8 consecutive outputs, at any element address.
+__device__ __forceinline__ void store_run(bf16_t* p, const float* f) {
+  typedef uint32_t word4 __attribute__((ext_vector_type(4), aligned(2)));
+  word4 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+  *(word4*)p = w;
+}
+__device__ __forceinline__ void store_run(float* p, const float* f) {
+  typedef float word4 __attribute__((ext_vector_type(4), aligned(4)));
+  word4 a, b;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) { a[j] = f[j]; b[j] = f[4 + j]; }
+  *(word4*)p = a;
+  *(word4*)(p + 4) = b;
+}
+
+// Where output (i, j .. j + 7) goes, with its bias.  positions: j runs over the
+// positions of all images, i over channels (channels first); else row-major.
+template <typename T>
+__device__ __forceinline__ void put_run(const Pw8Out& o, T* out, int64_t i, int64_t j, float* f) {
+  const int64_t left = o.cols - j;
+  if (o.bias) {
+    if (o.positions) {
+      const float b = Elem<T>::to_f32(((const T*)o.bias)[i]);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) f[u] += b;
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (u < left) f[u] += Elem<T>::to_f32(((const T*)o.bias)[j + u]);
+    }
+  }
+  int64_t at = i * o.cols + j, room = left;
+  if (o.positions) {
+    const int64_t image = (uint32_t)j / (uint32_t)o.positions, pos = j - image * o.positions;
+    at = (image * o.rows + i) * o.positions + pos;
+    if (o.positions - pos < room) room = o.positions - pos;
+  }
+  if (room >= 8) {
+    store_run(out + at, f);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    if (u < left) {
+      int64_t p = at + u;
+      if (o.positions) {
+        const int64_t image = (uint32_t)(j + u) / (uint32_t)o.positions;
+        p = (image * o.rows + i) * o.positions + (j + u - image * o.positions);
+      }
+      out[p] = Elem<T>::from_f32(f[u]);
+    }
+}
+
+// One workgroup of 2 x 2 waves computes BM x BN outputs over a range of blocks.
+//
+// Stages are half blocks (64 bytes of each row, and the block's scale bytes), in
+// a ring of four filled by loads straight into LDS; the fragments of the next
+// stage are read while the matrix instructions of the current one run, so one
+// wave a SIMD keeps its matrix unit fed.  16-byte pieces are XOR-swizzled: the
+// 16 rows of a read's phase lie in 16 places of a 256-byte bank window.
+template <int BM, int BN>
+struct Pw8Tile {
+  static constexpr int MI = BM / 64, NI = BN / 64;      // 32 x 32 blocks of a wave
+  static constexpr int kLoads = BM / 64 + BN / 64 + 1;  // of a wave, per stage; 1: scale bytes
+  static constexpr int kScaleBytes = 1024;              // of A, of B, and 512 that nobody reads
+  static constexpr int kStage = (BM + BN) * kHalf + kScaleBytes;
+  static constexpr int kRing = 4;
+  static constexpr int kEpiPitch = NI * 32 * 4 + 16;    // 32 rows of a wave's columns in fp32
+  static constexpr int kLds = kRing * kStage > 4 * 32 * kEpiPitch ? kRing * kStage : 4 * 32 * kEpiPitch;
+};
+
+template <typename T, int BM, int BN, bool PARTIAL>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 128 * 256 ? 1 : 2))) void k_pw8_gemm(
+    const Pw8GemmArgs g) {
+  using C = Pw8Tile<BM, BN>;
+  constexpr int MI = C::MI, NI = C::NI;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+
+  // tiles in bands of kBand rows of tiles, so that the tiles of an XCD share
+  // rows of both matrices in its L2
+  constexpr int kBand = 8;
+  const int id = xcd_swizzle(blockIdx.x, gridDim.x);
+  const int tiles = g.tiles_m * g.tiles_n;
+  const int split = uniform(id / tiles), in = id - split * tiles;
+  const int band = uniform(in / (kBand * g.tiles_n)), rows = min(kBand, g.tiles_m - band * kBand);
+  const int at = in - band * kBand * g.tiles_n;
+  const int tn = uniform(at / rows), tm = band * kBand + at - tn * rows;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int kb0 = split * g.per_split, kb1 = min(g.blocks, kb0 + g.per_split);
+  const int stages = 2 * (kb1 - kb0);
+
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // 16 rows of 64 bytes a load; a piece's place in its row depends on the row
+  const int lrow = lane >> 2;
+  const int voff = lrow * 128 + (((lane & 3) ^ ((lrow >> 2) & 3)) << 4);
+  const int64_t ra = g.a.rows - m0, rb = g.b.rows - n0;
+  const uint32_t bytes_a = uniform((uint32_t)min<int64_t>(ra, BM) * 128u);
+  const uint32_t bytes_b = uniform((uint32_t)min<int64_t>(rb, BN) * 128u);
+  const int64_t sa = pw8_scale_rows(g.a.rows), sb = pw8_scale_rows(g.b.rows);
+  const uint32_t scales_a = uniform((uint32_t)min<int64_t>(sa - m0, 256));
+  const uint32_t scales_b = uniform((uint32_t)min<int64_t>(sb - n0, 256));
+  const uint32_t lds0 = lds_addr_of(smem);
+
+  const uint64_t step_a = uniform64(g.a.rows * 128), step_b = uniform64(g.b.rows * 128);
+  uint64_t code_a = uniform64((uint64_t)(g.a.codes + (kb0 * g.a.rows + m0) * 128));
+  uint64_t code_b = uniform64((uint64_t)(g.b.codes + (kb0 * g.b.rows + n0) * 128));
+  // the scales that this wave loads: even waves A's, odd ones B's
+  uint64_t scale = uniform64((uint64_t)(wave & 1 ? g.b.scales + kb0 * sb + n0 : g.a.scales + kb0 * sa + m0));
+  const uint64_t step_s = uniform64(wave & 1 ? sb : sa);
+  const uint32_t bytes_s = wave & 1 ? scales_b : scales_a;
+
+  auto issue = [&](int s) {  // called for one stage after the other
+    const uint32_t base = lds0 + (s & 3) * C::kStage;
+    const int half = (s & 1) * kHalf;
+    const rsrc_t pa = uniform_rsrc(code_a, bytes_a);
+    const rsrc_t pb = uniform_rsrc(code_b, bytes_b);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int b = wave * MI + i;
+      load_lds16_so(pa, base + b * 1024, voff, b * 2048 + half);
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int b = wave * NI + j;
+      load_lds16_so(pb, base + BM * kHalf + b * 1024, voff, b * 2048 + half);
+    }
+    // every wave issues as many loads, so that it can wait for a count of them
+    load_lds4(uniform_rsrc(scale, bytes_s), base + (BM + BN) * kHalf + wave * 256, lane * 4);
+    if (half) {
+      code_a += step_a;
+      code_b += step_b;
+      scale += step_s;
+    }
+  };
+
+  struct Frags {
+    pw8_codes_t a[MI], b[NI];
+    int sa[MI], sb[NI];
+  };
+  const int frow = lane & 31, fh = lane >> 5;
+  const int sw = (frow >> 2) & 3;
+  const int c0 = ((2 * fh) ^ sw) << 4, c1 = ((2 * fh + 1) ^ sw) << 4;
+  auto fragment = [&](const unsigned char* p) {
+    const uint4 lo = *(const uint4*)(p + c0), hi = *(const uint4*)(p + c1);
+    pw8_codes_t v;
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    return v;
+  };
+  auto read = [&](int s, Frags& f) {
+    const unsigned char* st = smem + (s & 3) * C::kStage;
+    const unsigned char* sc = st + (BM + BN) * kHalf;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int r = wm * MI * 32 + i * 32 + frow;
+      f.a[i] = fragment(st + r * kHalf);
+      f.sa[i] = sc[r];
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int r = wn * NI * 32 + j * 32 + frow;
+      f.b[j] = fragment(st + (BM + r) * kHalf);
+      f.sb[j] = sc[256 + r];
+    }
+  };
+  // the columns' operand first: a lane then holds 4 consecutive columns of a row
+  auto multiply = [&](const Frags& f) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        bf16x8_t wa[MI], wb[NI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) wa[i] = pw8_wide(f.a[i], u, f.sa[i]);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) wb[j] = pw8_wide(f.b[j], u, f.sb[j]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[j], f.a[i], acc[i][j], 0, 0, 0, f.sb[j], 0,
+                                                                    f.sa[i]);
+  };
+  constexpr int kReads = 3 * (MI + NI);
+  auto interleave = [&]() {
+#pragma unroll
+    for (int u = 0; u < MI * NI; ++u) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                              // matrix instructions
+      __builtin_amdgcn_sched_group_barrier(0x100, (kReads + MI * NI - 1) / (MI * NI), 0);  // LDS reads
+    }
+  };
+  auto wait_stage = [&](int later) {  // how many stages may still be under way
+    if (later >= 3) wait_vm<3 * C::kLoads>();
+    else if (later == 2) wait_vm<2 * C::kLoads>();
+    else if (later == 1) wait_vm<C::kLoads>();
+    else wait_vm<0>();
+  };
+
+  Frags f[2];
+#pragma unroll
+  for (int s = 0; s < C::kRing; ++s)
+    if (s < stages) issue(s);
+  if (stages > 0) {
+    wait_stage(min(C::kRing, stages) - 1);
+    __syncthreads();
+    read(0, f[0]);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): stage 0 is in registers
+  }
+  // one stage: wait for the next one, refill this one's place, read the next
+  // one's fragments under this one's products
+  auto step = [&](int s, const Frags& now, Frags& next) {
+    if (s + 1 < stages) {
+      wait_stage(min(s + C::kRing, stages) - 2 - s);
+      __syncthreads();
+      if (s + C::kRing < stages) issue(s + C::kRing);
+      read(s + 1, next);
+    }
+    multiply(now);
+    if (sizeof(T) == 2) interleave();
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+  };
+  for (int s = 0; s < stages; s += 2) {  // a block is two stages
+    step(s, f[0], f[1]);
+    step(s + 1, f[1], f[0]);
+  }
+  __syncthreads();
+
+  // out through LDS, 32 rows of the wave at a time, so that lanes next to each
+  // other store next to each other
+  unsigned char* mine = smem + wave * 32 * C::kEpiPitch;
+  constexpr int kRuns = NI * 32 / 8, kRowsAt = 64 / kRuns;
+  const int64_t mw = m0 + wm * MI * 32, nw = n0 + wn * NI * 32;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        *(float4*)(mine + frow * C::kEpiPitch + (j * 32 + 8 * q + 4 * fh) * 4) = v;
+      }
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+    for (int u = 0; u < 32 / kRowsAt; ++u) {
+      const int r = u * kRowsAt + lane / kRuns, c = (lane % kRuns) * 8;
+      const int64_t row = mw + i * 32 + r, col = nw + c;
+      if (row < g.out.rows && col < g.out.cols) {
+        float v[8];
+        const float4 lo = *(const float4*)(mine + r * C::kEpiPitch + c * 4);
+        const float4 hi = *(const float4*)(mine + r * C::kEpiPitch + c * 4 + 16);
+        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        if (PARTIAL) {
+          // rows of whole runs: cols is rounded up to 8
+          float* p = g.part + ((int64_t)split * g.out.rows + row) * g.part_cols + col;
+          *(float4*)p = lo;
+          *(float4*)(p + 4) = hi;
+        } else {
+          put_run<T>(g.out, (T*)g.out.p, row, col, v);
+        }
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+  }
+}
+
+// Sums of the splits in their order, with the bias.
+template <typename T>
+__global__ __launch_bounds__(256) void k_pw8_join(const Pw8Out o, const float* part, int splits, int part_cols) {
+  const int64_t runs = part_cols / 8;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= o.rows * runs) return;
+  const int64_t i = id / runs, j = (id - i * runs) * 8;
+  const float* p = part + i * part_cols + j;
+  const int64_t pitch = o.rows * part_cols;
+  float v[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v[u] = 0.f;
+  int s = 0;
+  for (; s + 4 <= splits; s += 4) {
+    float4 f[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      f[u][0] = *(const float4*)(p + (s + u) * pitch);
+      f[u][1] = *(const float4*)(p + (s + u) * pitch + 4);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[0] += f[u][0].x; v[1] += f[u][0].y; v[2] += f[u][0].z; v[3] += f[u][0].w;
+      v[4] += f[u][1].x; v[5] += f[u][1].y; v[6] += f[u][1].z; v[7] += f[u][1].w;
+    }
+  }
+  for (; s < splits; ++s) {
+    const float4 lo = *(const float4*)(p + s * pitch), hi = *(const float4*)(p + s * pitch + 4);
+    v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+    v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+  }
+  put_run<T>(o, (T*)o.p, i, j, v);
+}
+
+template <typename T, int BM, int BN>
+hipError_t gemm(const Pw8GemmArgs& g, hipStream_t st) {
+  const uint32_t blocks = (uint32_t)g.tiles_m * g.tiles_n * g.splits;
+  constexpr int lds = Pw8Tile<BM, BN>::kLds;
+  hipError_t e = hipFuncSetAttribute(g.part ? (const void*)k_pw8_gemm<T, BM, BN, true> : (const void*)k_pw8_gemm<T, BM, BN, false>,
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  if (g.part) {
+    DEFT_LAUNCH("pw8_gemm", (k_pw8_gemm<T, BM, BN, true>), dim3(blocks), dim3(256), lds, st, g);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t runs = g.out.rows * (g.part_cols / 8);
+    DEFT_LAUNCH("pw8_join", k_pw8_join<T>, dim3((uint32_t)((runs + 255) / 256)), dim3(256), 0, st, g.out, g.part, g.splits,
+                g.part_cols);
+  } else {
+    DEFT_LAUNCH("pw8_gemm", (k_pw8_gemm<T, BM, BN, false>), dim3(blocks), dim3(256), lds, st, g);
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t gemm_of(const Pw8GemmArgs& g, int bm, int bn, hipStream_t st) {
+  if (bm == 256 && bn == 256) return gemm<T, 256, 256>(g, st);
+  if (bm == 128 && bn == 128) return gemm<T, 128, 128>(g, st);
+  return gemm<T, 64, 128>(g, st);
+}
+
+}  // namespace
+
+hipError_t launch_pw8_gemm(const Pw8GemmArgs& g, int bm, int bn, int dtype, hipStream_t st) {
+  return dtype == DEFT_F32 ? gemm_of<float>(g, bm, bn, st) : gemm_of<bf16_t>(g, bm, bn, st);
+}
+
+}  // namespace deft
