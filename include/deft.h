@@ -447,6 +447,60 @@ int deft_grad_norm(const void* const* g, const int64_t* n, int count, int g_dtyp
  * count themselves in it. */
 size_t deft_grad_norm_workspace_bytes(int count);
 
+/* ---- Muon over a list of matrices ----
+ *
+ * Momentum steps whose updates have their singular values brought near 1.  A
+ * tensor is a matrix [rows][cols] (a convolution's weight: its output channels by
+ * all the rest); per matrix, with g its gradient (times the factor in control),
+ *   m = mu m + (1 - mu) g
+ *   u = mu m + (1 - mu) g  with nesterov, else m
+ *   X = u / max(|u|_F, eps), then `steps` times
+ *       G = X X^T,  X = (a I + b G + c G^2) X     with a, b, c = 3.4445, -4.7750, 2.0315
+ *   p = p (1 - lr weight_decay) - lr scale X
+ * (G from the smaller side).  m and p take one fp32 rounding per operation in this
+ * order, p is rounded once to its dtype.  X is computed with 22 bits for each
+ * factor and sums in fp32, as near to the formula's value as steps in fp32 are:
+ * 2e-6 of its root mean square for matrices of normal values, 3e-5 where most
+ * singular values are small (their part of an error grows by up to 3.4 a step).
+ * A zero direction leaves X zero; a NaN or an infinity in u makes all of p's
+ * matrix NaN, and no other's.  Calls repeat their bits. */
+typedef struct deft_muon_desc {
+  int p_dtype, g_dtype; /* enum deft_dtype of the weights and of the gradients */
+  int master;           /* 1 (bf16 weights only): fp32 masters are updated, the weights are their
+                           rounded copies and are only written */
+  int nesterov;         /* 0 or 1 */
+  int steps;            /* 1 to 32; 5 is usual */
+  double lr, momentum, eps; /* lr >= 0, 0 <= momentum < 1, eps >= 1e-30 */
+} deft_muon_desc;
+
+typedef struct deft_muon_tensor {
+  void* p;              /* weights, updated */
+  const void* g;        /* gradient */
+  float* m;             /* momentum, updated */
+  float* master;        /* fp32 master weights, updated (desc.master) */
+  int64_t rows, cols;
+  double weight_decay;  /* decoupled, >= 0 */
+  double scale;         /* of the update, such as sqrt(max(1, rows / cols)) */
+} deft_muon_tensor;
+
+/* Workspace bytes of deft_muon_step for this list (its shapes), on a device of as
+ * many compute units as the current one; 0 for a list that it refuses.  Nothing is
+ * kept in it from call to call. */
+size_t deft_muon_workspace_bytes(const deft_muon_tensor* t, int count);
+
+/* One step over all listed matrices.  Like deft_adamw_step it takes a host array,
+ * copies nothing to the device and can be captured; control (device, may be NULL)
+ * is what deft_grad_norm wrote: where it says that the gradients are not finite, the
+ * step writes nothing but its workspace.  schedule (device, may be NULL): one
+ * double, the lr that replaces the descriptor's, read when the kernels run.
+ * count = 0 and matrices of no elements are allowed.
+ * DEFT_ERR_DTYPE; DEFT_ERR_BAD_DESC (a negative size, a rate out of range, masters
+ * for fp32 weights); DEFT_ERR_UNSUPPORTED (a smaller side over 2^15, a larger one
+ * over 2^22, over 2^32 elements); DEFT_ERR_NULLPTR; DEFT_ERR_ALIGN (tensors and workspace 16 bytes,
+ * control 4, schedule 8); DEFT_ERR_WORKSPACE.  Checks run before any launch. */
+int deft_muon_step(const deft_muon_desc* d, const deft_muon_tensor* t, int count, const float* control,
+                   const double* schedule, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- Pointwise (1x1) convolution in 8 bits, with its gradients ----
  *
  * x is [n][c_in][s] (DEFT_CHANNELS_FIRST) or [n][s][c_in] (DEFT_CHANNELS_LAST),

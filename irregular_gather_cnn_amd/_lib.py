@@ -35,7 +35,7 @@ EXPORTED = ["deft_desc_validate", "deft_plan_create", "deft_plan_create_forced",
             "deft_norm_desc_validate", "deft_norm_workspace_bytes", "deft_norm_forward",
             "deft_norm_backward", "deft_debug_norm_patience", "deft_debug_norm_cut",
             "deft_pw8_desc_validate", "deft_pw8_packed_bytes", "deft_pw8_saved_bytes", "deft_pw8_workspace_bytes",
-            "deft_pw8_pack", "deft_pw8_forward", "deft_pw8_backward"]
+            "deft_pw8_pack", "deft_pw8_forward", "deft_pw8_backward", "deft_muon_workspace_bytes", "deft_muon_step"]
 LAYOUTS = {"channels_first": 0, "channels_last": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
@@ -81,6 +81,17 @@ class deft_adamw_tensor(ctypes.Structure):
 class deft_norm_desc(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int) for k in ("n", "c", "s", "groups", "layout", "act", "dtype")] + [
         ("eps", ctypes.c_double)]
+
+
+class deft_muon_desc(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int) for k in ("p_dtype", "g_dtype", "master", "nesterov", "steps")] + [
+        (k, ctypes.c_double) for k in ("lr", "momentum", "eps")]
+
+
+class deft_muon_tensor(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("p", "g", "m", "master")] + [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+        ("scale", ctypes.c_double)]
 
 
 class deft_pw8_desc(ctypes.Structure):
@@ -135,6 +146,8 @@ def load() -> ctypes.CDLL:
         "deft_pw8_pack": (i, [ctypes.POINTER(deft_pw8_desc), vp, vp, vp]),
         "deft_pw8_forward": (i, [ctypes.POINTER(deft_pw8_desc)] + [vp] * 6 + [sz, vp]),
         "deft_pw8_backward": (i, [ctypes.POINTER(deft_pw8_desc)] + [vp] * 7 + [sz, vp]),
+        "deft_muon_workspace_bytes": (sz, [vp, i]),
+        "deft_muon_step": (i, [ctypes.POINTER(deft_muon_desc), vp, i, vp, vp, vp, sz, vp]),
         "deft_error_string": (ctypes.c_char_p, [i]),
         "deft_last_hip_error": (ctypes.c_char_p, []),
         "deft_timing_start": (i, [i]),
@@ -312,6 +325,11 @@ def deft_pw8_saved_bytes(desc: deft_pw8_desc) -> int:
 
 def deft_pw8_workspace_bytes(desc: deft_pw8_desc) -> int:
     return int(load().deft_pw8_workspace_bytes(ctypes.byref(desc)))
+
+
+def deft_muon_workspace_bytes(tensors, count: int) -> int:
+    """tensors: an array of deft_muon_tensor."""
+    return int(load().deft_muon_workspace_bytes(tensors, int(count)))
 
 
 def deft_error_string(code: int) -> str:

@@ -295,4 +295,63 @@ struct Pw8FewArgs {
 };
 hipError_t launch_pw8_few(const Pw8FewArgs& a, int dtype, int cus, hipStream_t st);
 
+// Muon over a list of matrices (deft_muon.hip).  A matrix's share of the
+// workspace: X twice, kMuonSquares matrices of the smaller side, partial sums of
+// squares and of products.  X has the smaller side first (m <= n), so it is a tall
+// matrix's transpose.  Sides are rounded up to 32 with zeros (mp, np), values are
+// pairs of fp16 in two planes.
+constexpr int kMuonList = 48;      // matrices of a launch
+constexpr int kMuonPad = 32, kMuonSquares = 6, kMuonSums = 256;
+struct MuonItem {
+  char* base;                      // its share of the workspace
+  void* p;
+  const void* g;
+  float* mom;
+  float* master;
+  double decay;                    // weight decay
+  double scale;                    // of the update, lr apart
+  int m, n;
+  int tall;                        // p is [n][m]
+  int splits;                      // of the sum over n
+};
+struct MuonArgs {
+  MuonItem it[kMuonList];
+  uint32_t first[kMuonList];       // first workgroup of each matrix
+  int count;
+  float mu, nu;                    // momentum and 1 - momentum
+  int nesterov;
+  double eps, lr;
+  const float* control;            // nullable
+  const double* schedule;          // nullable
+  // products: out = f A B + fd I + fb add, by numbers of buffers: 0 and 1 are X, the others squares
+  struct Phase {
+    int a, b, out, add;
+    float f, fd, fb;
+  } ph[2];
+};
+static_assert(sizeof(MuonArgs) <= 4096, "kernel arguments");
+__host__ __device__ inline int64_t muon_pad(int64_t v) { return (v + kMuonPad - 1) / kMuonPad * kMuonPad; }
+__host__ __device__ inline int64_t muon_x_bytes(int m, int n) { return 4 * muon_pad(m) * muon_pad(n); }
+__host__ __device__ inline int64_t muon_square_bytes(int m) { return 4 * muon_pad(m) * muon_pad(m); }
+__host__ __device__ inline int64_t muon_buffer(int id, int m, int n) {
+  return id < 2 ? id * muon_x_bytes(m, n) : 2 * muon_x_bytes(m, n) + (id - 2) * muon_square_bytes(m);
+}
+__host__ __device__ inline int64_t muon_sums(int m, int n) { return muon_buffer(2 + kMuonSquares, m, n); }
+__host__ __device__ inline int64_t muon_parts(int m, int n) { return muon_sums(m, n) + kMuonSums * 8; }
+inline int64_t muon_item_bytes(int m, int n, int splits) {
+  return (muon_parts(m, n) + (splits > 1 ? splits * muon_square_bytes(m) : 0) + 255) / 256 * 256;
+}
+// Elements whose squares a workgroup sums, at most kMuonSums workgroups a matrix.
+inline int64_t muon_chunk(int64_t n) {
+  const int64_t least = 4096, c = (n + kMuonSums - 1) / kMuonSums;
+  return c <= least ? least : (c + 1023) / 1024 * 1024;
+}
+hipError_t launch_muon_momentum(const MuonArgs& a, uint32_t blocks, int g_dtype, hipStream_t st);
+hipError_t launch_muon_scale(const MuonArgs& a, uint32_t blocks, int g_dtype, hipStream_t st);
+// tile: 64 or 128; phases: 1 or 2 products in one launch
+hipError_t launch_muon_square(const MuonArgs& a, uint32_t blocks, int tile, int phases, bool split, hipStream_t st);
+hipError_t launch_muon_join(const MuonArgs& a, uint32_t blocks, hipStream_t st);
+hipError_t launch_muon_apply(const MuonArgs& a, uint32_t blocks, int tile, bool last, int p_dtype, bool master,
+                             hipStream_t st);
+
 }  // namespace deft

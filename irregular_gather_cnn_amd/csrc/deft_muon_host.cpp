@@ -1,0 +1,266 @@
+// C ABI of the Muon step: argument checks, the matrices' shares of the workspace
+// and the sequence of launches.  Kernels live in deft_muon.hip.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "deft.h"
+#include "deft_internal.h"
+
+namespace {
+
+// Smaller and larger side, and elements: tiles are counted and offsets inside them
+// made in 32 bits.
+constexpr int64_t kMaxSide = 1 << 15, kMaxLong = 1 << 22, kMaxElems = (int64_t)1 << 32;
+constexpr int64_t kChunkBytes = (int64_t)2 << 30;          // workspace, but for single matrices that need more
+constexpr int kMaxSteps = 32;
+constexpr int kFused = 3;  // steps between two products with X
+
+// Newton-Schulz coefficients: sigma -> a sigma + b sigma^3 + c sigma^5 takes
+// singular values of (0, 1] to 0.68 .. 1.21 in five steps where they were over 0.002.
+constexpr double kA = 3.4445, kB = -4.7750, kC = 2.0315;
+// Powers of two by which X and G, Q and P are held (deft_muon.hip).
+constexpr double kSx = 16384.0, kSg = 16384.0, kSq = 8192.0, kSp = 1024.0;
+
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool dtype_ok(int t) { return t == DEFT_F32 || t == DEFT_BF16; }
+int status_of(hipError_t e) { return e == hipSuccess ? DEFT_OK : deft::report_hip_error(e); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int shape_status(const deft_muon_tensor& t) {
+  if (t.rows < 0 || t.cols < 0) return DEFT_ERR_BAD_DESC;
+  if (t.rows == 0 || t.cols == 0) return DEFT_OK;
+  if (std::min(t.rows, t.cols) > kMaxSide || std::max(t.rows, t.cols) > kMaxLong || t.rows * t.cols > kMaxElems)
+    return DEFT_ERR_UNSUPPORTED;
+  return DEFT_OK;
+}
+
+int64_t triangle(int64_t tiles) { return tiles * (tiles + 1) / 2; }
+int64_t square_tiles(int m, int tile) { return triangle(ceil_div(deft::muon_pad(m), tile)); }
+
+// Matrices whose launches go together: first and number in the list, their shape
+// and shares of the workspace.
+struct Chunk {
+  deft::MuonItem it[deft::kMuonList];
+  int id[deft::kMuonList];
+  int count = 0, next = 0;  // next: where in the list the following chunk starts
+  bool split = false;
+  int64_t bytes = 0;
+};
+
+// Tile of the products of squares: 128 where that gives every compute unit one.
+int square_tile(const Chunk& c, int cus) {
+  int64_t n = 0;
+  for (int i = 0; i < c.count; ++i) n += square_tiles(c.it[i].m, 128);
+  return n >= cus ? 128 : 64;
+}
+int64_t apply_tiles(int m, int n, int tile) {
+  return ceil_div(deft::muon_pad(m), tile) * ceil_div(deft::muon_pad(n), tile);
+}
+int apply_tile(const Chunk& c, int cus) {
+  int64_t n = 0;
+  for (int i = 0; i < c.count; ++i) n += apply_tiles(c.it[i].m, c.it[i].n, 128);
+  return n >= cus / 2 ? 128 : 64;
+}
+
+// The next chunk of the list from `at` on; its items' shares start at `base`.
+void next_chunk(const deft_muon_tensor* t, int count, int at, int cus, char* base, Chunk& c) {
+  c.count = 0;
+  c.bytes = 0;
+  int64_t most = 0;
+  for (c.next = at; c.next < count && c.count < deft::kMuonList; ++c.next) {
+    const deft_muon_tensor& x = t[c.next];
+    if (x.rows == 0 || x.cols == 0) continue;
+    deft::MuonItem& y = c.it[c.count];
+    y.m = (int)std::min(x.rows, x.cols);
+    y.n = (int)std::max(x.rows, x.cols);
+    y.tall = x.rows > x.cols;
+    y.splits = 1;
+    const int64_t need = deft::muon_item_bytes(y.m, y.n, 1);
+    if (c.count && most + need > kChunkBytes) break;
+    most += need;
+    c.id[c.count++] = c.next;
+  }
+  // the sums over n are split where their tiles leave compute units idle, into no
+  // fewer than 4 stages
+  const int tile = square_tile(c, cus);
+  int64_t tiles = 0;
+  for (int i = 0; i < c.count; ++i) tiles += square_tiles(c.it[i].m, tile);
+  const int64_t splits = tiles ? std::max<int64_t>(1, 2 * cus / tiles) : 1;
+  c.split = false;
+  for (int i = 0; i < c.count; ++i) {
+    c.it[i].splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, deft::muon_pad(c.it[i].n) / (4 * deft::kMuonPad)));
+    c.split |= c.it[i].splits > 1;
+  }
+  for (int i = 0; i < c.count; ++i) {
+    c.it[i].base = base + c.bytes;
+    c.bytes += deft::muon_item_bytes(c.it[i].m, c.it[i].n, c.split ? std::max(2, c.it[i].splits) : 1);
+  }
+}
+
+// Sets the first workgroups of the items, `of` each; the sum.
+template <typename F>
+uint32_t lay(deft::MuonArgs& a, F of) {
+  int64_t at = 0;
+  for (int i = 0; i < a.count; ++i) {
+    a.first[i] = (uint32_t)at;
+    at += of(a.it[i]);
+  }
+  return (uint32_t)at;
+}
+
+struct Launcher {
+  deft::MuonArgs& a;
+  int tile, wide, p_dtype;
+  bool split, master;
+  hipStream_t st;
+  hipError_t e = hipSuccess;
+
+  void gram(int x, int out) {
+    if (e != hipSuccess) return;
+    a.ph[0] = {x, x, out, -1, (float)(kSg / (kSx * kSx)), 0.f, 0.f};
+    const int t = tile;
+    const bool s = split;
+    const uint32_t n = lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, t) * (s ? i.splits : 1); });
+    e = deft::launch_muon_square(a, n, tile, 1, split, st);
+    if (e != hipSuccess || !split) return;
+    e = deft::launch_muon_join(a, lay(a, [](const deft::MuonItem& i) { return square_tiles(i.m, 32); }), st);
+  }
+  void squares(int phases) {
+    if (e != hipSuccess) return;
+    const int t = tile;
+    e = deft::launch_muon_square(a, lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, t); }), tile, phases,
+                                 false, st);
+  }
+  void apply(int p, double scale, int x, int out, bool last) {
+    if (e != hipSuccess) return;
+    a.ph[0] = {p, x, out, -1, (float)(last ? 1.0 / (scale * kSx) : 1.0 / scale), 0.f, 0.f};
+    const int t = wide;
+    e = deft::launch_muon_apply(a, lay(a, [&](const deft::MuonItem& i) { return apply_tiles(i.m, i.n, t); }), wide, last,
+                                p_dtype, master, st);
+  }
+
+  // `steps` <= 3 of them on the X in buffer x; the result goes to the other one, or to the weights.
+  void fused(int steps, int x, bool last) {
+    int g = 2, other = 5, p = -1;
+    double scale = kSq;
+    const int r = 6;
+    gram(x, g);
+    for (int k = 0; k < steps; ++k) {
+      // buffers of the squares: G 2 and 5 in turn, R 6, Q and P 3, 4, 7
+      const int q = k == 1 ? 4 : 3, to = k == 1 ? 7 : 4;
+      a.ph[0] = {g, g, q, g, (float)(kC * kSq / (kSg * kSg)), (float)(kA * kSq), (float)(kB * kSq / kSg)};
+      squares(1);
+      int n = 0;
+      if (k > 0) {
+        a.ph[n++] = {q, p, to, -1, (float)(k == 1 ? kSp / (kSq * kSq) : 1.0 / kSq), 0.f, 0.f};
+        scale = kSp;
+      }
+      p = k > 0 ? to : q;
+      if (k + 1 < steps) a.ph[n++] = {q, g, r, -1, (float)(1.0 / kSq), 0.f, 0.f};
+      if (n) squares(n);
+      if (k + 1 < steps) {
+        a.ph[0] = {q, r, other, -1, (float)(1.0 / kSq), 0.f, 0.f};
+        squares(1);
+        std::swap(g, other);
+      }
+    }
+    apply(p, scale, x, 1 - x, last);
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t deft_muon_workspace_bytes(const deft_muon_tensor* t, int count) {
+  if (count <= 0 || !t) return 0;
+  for (int i = 0; i < count; ++i)
+    if (shape_status(t[i]) != DEFT_OK) return 0;
+  int64_t most = 0;
+  Chunk c;
+  const int cus = deft::compute_units();
+  for (int at = 0; at < count; at = c.next) {
+    next_chunk(t, count, at, cus, nullptr, c);
+    most = std::max(most, c.bytes);
+  }
+  return (size_t)most;
+}
+
+int deft_muon_step(const deft_muon_desc* d, const deft_muon_tensor* t, int count, const float* control,
+                   const double* schedule, void* workspace, size_t ws_bytes, void* stream) {
+  if (!d || (count > 0 && !t)) return DEFT_ERR_NULLPTR;
+  if (!dtype_ok(d->p_dtype) || !dtype_ok(d->g_dtype)) return DEFT_ERR_DTYPE;
+  // negated comparisons refuse NaN
+  if (count < 0 || d->steps < 1 || d->steps > kMaxSteps || (d->nesterov != 0 && d->nesterov != 1) || !(d->lr >= 0.0) ||
+      !std::isfinite(d->lr) || !(d->momentum >= 0.0 && d->momentum < 1.0) || !(d->eps >= 1e-30) || !std::isfinite(d->eps) ||
+      (d->master != 0 && d->master != 1) || (d->master && d->p_dtype == DEFT_F32))
+    return DEFT_ERR_BAD_DESC;
+  if (!aligned(control, 4) || !aligned(schedule, 8)) return DEFT_ERR_ALIGN;
+  for (int i = 0; i < count; ++i) {
+    const deft_muon_tensor& x = t[i];
+    const int st = shape_status(x);
+    if (st != DEFT_OK) return st;
+    if (!(x.weight_decay >= 0.0) || !std::isfinite(x.weight_decay) || !std::isfinite(x.scale)) return DEFT_ERR_BAD_DESC;
+    if (x.rows == 0 || x.cols == 0) continue;
+    if (!x.p || !x.g || !x.m || (d->master && !x.master)) return DEFT_ERR_NULLPTR;
+    if (!aligned(x.p, 16) || !aligned(x.g, 16) || !aligned(x.m, 16) || (d->master && !aligned(x.master, 16)))
+      return DEFT_ERR_ALIGN;
+  }
+  const size_t need = deft_muon_workspace_bytes(t, count);
+  if (need && (!workspace || ws_bytes < need)) return DEFT_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DEFT_ERR_ALIGN;
+  const int cus = deft::compute_units();
+  const hipStream_t st = (hipStream_t)stream;
+  Chunk c;
+  for (int at = 0; at < count; at = c.next) {
+    next_chunk(t, count, at, cus, (char*)workspace, c);
+    if (!c.count) continue;
+    deft::MuonArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.count = c.count;
+    a.mu = (float)d->momentum;
+    a.nu = (float)(1.0 - d->momentum);
+    a.nesterov = d->nesterov;
+    a.eps = d->eps;
+    a.lr = d->lr;
+    a.control = control;
+    a.schedule = schedule;
+    for (int i = 0; i < c.count; ++i) {
+      const deft_muon_tensor& x = t[c.id[i]];
+      deft::MuonItem& y = a.it[i] = c.it[i];
+      y.p = x.p;
+      y.g = x.g;
+      y.mom = x.m;
+      y.master = x.master;
+      y.decay = x.weight_decay;
+      y.scale = x.scale;
+    }
+    hipError_t e = deft::launch_muon_momentum(
+        a, lay(a, [](const deft::MuonItem& i) {
+          const int64_t n = (int64_t)i.m * i.n;
+          return ceil_div(n, deft::muon_chunk(n));
+        }), d->g_dtype, st);
+    if (e == hipSuccess)
+      e = deft::launch_muon_scale(
+          a, lay(a, [](const deft::MuonItem& i) { return ceil_div(deft::muon_pad(i.m), 64) * ceil_div(deft::muon_pad(i.n), 64); }),
+          d->g_dtype, st);
+    if (e != hipSuccess) return status_of(e);
+    Launcher l{a, square_tile(c, cus), apply_tile(c, cus), d->p_dtype, c.split, d->master != 0, st};
+    // as few parts of at most kFused steps as there may be, the larger ones first
+    int parts = (d->steps + kFused - 1) / kFused, left = d->steps, x = 0;
+    for (; parts > 0; --parts) {
+      const int k = (left + parts - 1) / parts;
+      l.fused(k, x, parts == 1);
+      x = 1 - x;
+      left -= k;
+    }
+    if (l.e != hipSuccess) return status_of(l.e);
+  }
+  return DEFT_OK;
+}
+
+}  // extern "C"

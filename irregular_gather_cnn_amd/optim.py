@@ -1,12 +1,15 @@
-"""The end of a training step: gradient norm and AdamW over a list of tensors.
+"""The end of a training step: gradient norm, AdamW over a list of tensors, and
+Muon over a list of matrices.
 
 PyTorch only supplies device memory and the stream; the arithmetic runs in
-libdeft.so (``deft_grad_norm``, ``deft_adamw_step``) through the binding in
-``_lib``.
+libdeft.so (``deft_grad_norm``, ``deft_adamw_step``, ``deft_muon_step``) through
+the binding in ``_lib``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import struct
 
 import torch
@@ -226,3 +229,115 @@ class AdamW:
         if code:
             raise _lib.DeftError(code, "deft_adamw_step")
         self.steps += 1
+
+
+# the factor of an update, lr apart, from a matrix's rows and columns
+ADJUST = {
+    "none": lambda rows, cols: 1.0,
+    # an update of a tall matrix as large, for inputs of one size, as a square one's
+    "aspect": lambda rows, cols: math.sqrt(max(1.0, rows / cols)),
+    # an update of root mean square 0.2, about AdamW's, whose lr and decay then serve both
+    "rms": lambda rows, cols: 0.2 * math.sqrt(max(rows, cols)),
+}
+
+
+class Muon:
+    """Momentum steps whose updates have their singular values brought near 1 by
+    ``steps`` Newton-Schulz steps, over ``params`` (device tensors of two or more
+    dimensions, all float32 or all bfloat16, updated in place; a matrix is the
+    first dimension by all others, as a convolution's weight is) and their gradient
+    buffers ``grads`` (likewise; read at every step, :meth:`bind` names others).
+    Biases and other vectors are for :class:`AdamW`.
+
+    ``adjust``: the update's factor besides lr: "none", "aspect" (sqrt(max(1,
+    rows / cols))) or "rms" (0.2 sqrt(max(rows, cols))).  ``masters``: None, True
+    (fp32 copies of bfloat16 params are made and updated, params are their rounded
+    copies) or a list of fp32 tensors.  ``weight_decay``: one number or one per
+    tensor.  ``states``: None (zeros) or a list of float32 momenta, updated in
+    place, as :attr:`states` of an earlier run.
+
+    The addresses of all tensors are taken here and in :meth:`bind`, and that
+    memory is held: a tensor that is given other memory later on (``p.data =
+    ...``) needs a new handle, a gradient a new :meth:`bind`.  Steps of one handle
+    on several streams must be ordered by the caller, as they share a workspace."""
+
+    def __init__(self, params, grads, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.01, steps=5,
+                 adjust="aspect", eps=1e-7, masters=None, states=None):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no params")
+        if adjust not in ADJUST:
+            raise ValueError("adjust must be one of %s, got %r" % (sorted(ADJUST), adjust))
+        self.device, self.index = self.params[0].device, self.params[0].get_device()
+        p_dtype = _dtype_of(self.params, "params")
+        for p in self.params:
+            _dense(p, "a param", self.index)
+            if p.dim() < 2:
+                raise ValueError("a param must have two dimensions or more, got %d" % p.dim())
+        self.sizes = [p.numel() for p in self.params]
+        self.shapes = [(p.shape[0], math.prod(p.shape[1:])) for p in self.params]
+        self.grads = _Gradients(grads)
+        if self.grads.sizes != self.sizes or self.grads.device != self.device:
+            raise ValueError("the gradients' sizes and device must be those of the params")
+        if masters is True:
+            masters = [p.float() for p in self.params]
+        self.masters = list(masters) if masters else None
+        self.states = list(states) if states is not None else [
+            torch.zeros(n, dtype=torch.float32, device=self.device) for n in self.sizes]
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(self.params)
+        for what, got in (("masters", self.masters), ("states", self.states), ("weight decays", decay)):
+            if got is not None and len(got) != len(self.params):
+                raise ValueError("%d %s for %d params" % (len(got), what, len(self.params)))
+        for k, n in enumerate(self.sizes):
+            for what, held in (("state", self.states), ("master", self.masters)):
+                if held is not None:
+                    if held[k] is None or held[k].numel() != n or held[k].dtype != torch.float32:
+                        raise ValueError("%s %d must have %d elements of torch.float32" % (what, k, n))
+                    _dense(held[k], "%s %d" % (what, k), self.index)
+        self.lr = lr
+        self._desc = _lib.deft_muon_desc(p_dtype, self.grads.dtype, 1 if self.masters else 0, 1 if nesterov else 0, steps,
+                                         lr, momentum, eps)
+        self._list = (_lib.deft_muon_tensor * len(self.params))()
+        for k, (item, p) in enumerate(zip(self._list, self.params)):
+            rows, cols = self.shapes[k]
+            item.p, item.g, item.m = p.data_ptr(), self.grads.pointers[k], self.states[k].data_ptr()
+            item.master = self.masters[k].data_ptr() if self.masters else None
+            item.rows, item.cols, item.weight_decay = rows, cols, decay[k]
+            item.scale = ADJUST[adjust](rows, cols) if rows and cols else 1.0
+        with torch.cuda.device(self.index) if elsewhere(self.index) else contextlib.nullcontext():
+            self.ws_bytes = _lib.deft_muon_workspace_bytes(self._list, len(self.params))
+        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        self._held = _hold(self.params + (self.masters or []) + self.states)
+        self._call, self._ref, self._ws = _lib.load().deft_muon_step, ctypes.byref(self._desc), self.ws.data_ptr()
+        self._norm = GradNorm.__new__(GradNorm)
+        self._norm._setup(self.grads)
+
+    def bind(self, grads):
+        """From now on the gradients are read from these tensors."""
+        self.grads.bind(grads)
+        for item, g in zip(self._list, self.grads.pointers):
+            item.g = g
+
+    def grad_norm(self, max_norm=float("inf"), inv_scale=1.0):
+        """``control`` of the gradients (see :class:`GradNorm`), for :meth:`step`."""
+        return self._norm(max_norm, inv_scale)
+
+    def step(self, control=None, lr=None, schedule=None):
+        """One step.  ``control``: what :meth:`grad_norm`, or a :class:`GradNorm` over more gradients than
+        these, returned; its factor multiplies the gradients and the step writes nothing if they are not
+        finite.  ``lr``: from now on.  ``schedule``: one device double, the lr that the kernels read in place
+        of the host's, for a step captured in a graph."""
+        if lr is not None:
+            self.lr = lr
+        for what, t, n, kind in (("control", control, 4, torch.float32), ("schedule", schedule, 1, torch.float64)):
+            if t is not None and (t.numel() != n or t.dtype != kind or t.device != self.device or not t.is_contiguous()):
+                raise ValueError("%s must be %d contiguous elements of %s on %s" % (what, n, kind, self.device))
+        if elsewhere(self.index):
+            with torch.cuda.device(self.index):
+                return self.step(control, lr, schedule)
+        self._desc.lr = self.lr
+        code = self._call(self._ref, self._list, len(self.params), None if control is None else control.data_ptr(),
+                          None if schedule is None else schedule.data_ptr(), self._ws, self.ws_bytes,
+                          current_stream(self.index))
+        if code:
+            raise _lib.DeftError(code, "deft_muon_step")
