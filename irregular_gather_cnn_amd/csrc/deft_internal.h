@@ -243,9 +243,13 @@ hipError_t launch_norm_params(const float* part, int rows, int c, void* dgamma, 
                               hipStream_t st);
 
 // Pointwise convolution in 8 bits (deft_pw8_quantise.hip, deft_pw8_gemm.hip,
-// deft_pw8_few.hip).  A matrix of codes over `rows` and a depth, stored by blocks
-// of 128 of the depth: codes [blocks][rows][128], scales [blocks][pw8_scale_rows].
-constexpr int kPw8Block = 128;
+// deft_pw8_few.hip).  A matrix of codes over `rows` and a depth, stored by half
+// blocks: codes [blocks][2][rows][64], scales [blocks][pw8_scale_rows].
+constexpr int kPw8Block = DEFT_PW8_BLOCK;
+// Where the 64 codes of a row's half of a block start.
+__host__ __device__ inline int64_t pw8_code(int64_t block, int half, int64_t rows, int64_t row) {
+  return ((block * 2 + half) * rows + row) * (kPw8Block / 2);
+}
 __host__ __device__ inline int64_t pw8_scale_rows(int64_t rows) { return (rows + 15) & ~(int64_t)15; }
 struct Pw8Matrix {
   const uint8_t* codes;

@@ -5,6 +5,13 @@
 // the nearest e4m3, ties to even; the block's scale byte is e + 127.  A NaN or an
 // infinity becomes the code NaN, and so reaches the outputs that it enters and
 // no other.
+//
+// A matrix of codes over rows and a depth is stored by half blocks of the depth:
+// codes [ceil(depth / 128)][2][rows][64], the last block filled up with zeros, and
+// scale bytes [ceil(depth / 128)][round_up(rows, 16)].  What a stage of a product
+// reads is then one piece of memory, in whole lines (with 128 codes of a row in
+// sequence a stage read half lines: 8192^3 took 571 us where it takes 530), and
+// offsets inside it fit 32 bits however large the matrix is.
 #pragma once
 #include "deft_device.h"
 

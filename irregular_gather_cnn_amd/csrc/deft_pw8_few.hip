@@ -3,7 +3,7 @@
 //
 // One launch: y[r][o] = sum_k x[r][k] w[o][k] + b[o].  A workgroup takes 16 or 32
 // outputs o, its waves share the blocks of k.  A wave reads a block of its
-// weights as they lie (2 KB for 16 outputs) and 32 values of a row of x a lane,
+// weights as they lie (twice 1 KB for 16 outputs) and 32 values of a row of x a lane,
 // which it turns into codes by itself, in the registers that the matrix
 // instruction takes them from; the blocks' codes are those that the quantising
 // launch makes.  The waves' sums meet in LDS, in their order.
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_pw8_few(const Pw8FewArgs a) {
         for (int f = 0; f < NF; ++f) {
           // rows beyond the last are the last one's: their outputs are not stored
           const int64_t o = min(o0 + f * 16 + row, a.w.rows - 1);
-          const uint8_t* p = a.w.codes + ((int64_t)kb * a.w.rows + o) * kPw8Block + h * 32;
+          const uint8_t* p = a.w.codes + pw8_code(kb, h >> 1, a.w.rows, o) + (h & 1) * 32;
           lo[u][f] = *(const uint4*)p;
           hi[u][f] = *(const uint4*)(p + 16);
           ws[u][f] = a.w.scales[kb * spitch + o];

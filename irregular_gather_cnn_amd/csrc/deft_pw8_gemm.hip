@@ -2,12 +2,13 @@
 // and its gradients.
 //
 // C[i][j] = sum_k A[i][k] B[j][k] over two matrices of e4m3 codes stored by
-// blocks of 128 of k (deft_pw8_quantise.hip), each row of a block with a power
-// of two.  v_mfma_scale_f32_32x32x64 multiplies 64 codes of 32 rows by 64 of 32
+// half blocks of 64 of k (deft_pw8.h), each row of a block of 128 with a power of
+// two.  v_mfma_scale_f32_32x32x64 multiplies 64 codes of 32 rows by 64 of 32
 // others, with their powers of two, into fp32: twice the rate of bf16, and no
 // vector operations for the scales.  Products for fp32 results are 16-bit ones
 // (deft_pw8.h says why).
 #include <algorithm>
+#include <type_traits>
 
 #include "deft_device.h"
 #include "deft_internal.h"
@@ -101,15 +102,16 @@ __device__ __forceinline__ void put_run(const Pw8Out& o, T* out, int64_t i, int6
 
 // One workgroup of 2 x 2 waves computes BM x BN outputs over a range of blocks.
 //
-// Stages are half blocks (64 bytes of each row, and the block's scale bytes), in
-// a ring of four filled by loads straight into LDS; the fragments of the next
-// stage are read while the matrix instructions of the current one run, so one
-// wave a SIMD keeps its matrix unit fed.  16-byte pieces are XOR-swizzled: the
+// Stages are half blocks (64 bytes of each row; the first half with the block's
+// scale bytes), in a ring of four filled by loads straight into LDS.  The
+// fragments of the next stage are read, and a later one's loads issued, one or two
+// between two matrix instructions, so one wave a SIMD keeps its matrix unit fed.
+// 16-byte pieces are XOR-swizzled: the
 // 16 rows of a read's phase lie in 16 places of a 256-byte bank window.
 template <int BM, int BN>
 struct Pw8Tile {
   static constexpr int MI = BM / 64, NI = BN / 64;      // 32 x 32 blocks of a wave
-  static constexpr int kLoads = BM / 64 + BN / 64 + 1;  // of a wave, per stage; 1: scale bytes
+  static constexpr int kLoads = BM / 64 + BN / 64;      // of a wave, per stage, and one for a block's scale bytes
   static constexpr int kScaleBytes = 1024;              // of A, of B, and 512 that nobody reads
   static constexpr int kStage = (BM + BN) * kHalf + kScaleBytes;
   static constexpr int kRing = 4;
@@ -149,51 +151,53 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
 
   // 16 rows of 64 bytes a load; a piece's place in its row depends on the row
   const int lrow = lane >> 2;
-  const int voff = lrow * 128 + (((lane & 3) ^ ((lrow >> 2) & 3)) << 4);
+  const int voff = lrow * kHalf + (((lane & 3) ^ ((lrow >> 2) & 3)) << 4);
   const int64_t ra = g.a.rows - m0, rb = g.b.rows - n0;
-  const uint32_t bytes_a = uniform((uint32_t)min<int64_t>(ra, BM) * 128u);
-  const uint32_t bytes_b = uniform((uint32_t)min<int64_t>(rb, BN) * 128u);
-  const int64_t sa = pw8_scale_rows(g.a.rows), sb = pw8_scale_rows(g.b.rows);
-  const uint32_t scales_a = uniform((uint32_t)min<int64_t>(sa - m0, 256));
-  const uint32_t scales_b = uniform((uint32_t)min<int64_t>(sb - n0, 256));
+  const uint32_t bytes_a = uniform((uint32_t)min<int64_t>(ra, BM) * (uint32_t)kHalf);
+  const uint32_t bytes_b = uniform((uint32_t)min<int64_t>(rb, BN) * (uint32_t)kHalf);
+  const int64_t srows_a = pw8_scale_rows(g.a.rows), srows_b = pw8_scale_rows(g.b.rows);
+  const uint32_t scales_a = uniform((uint32_t)min<int64_t>(srows_a - m0, 256));
+  const uint32_t scales_b = uniform((uint32_t)min<int64_t>(srows_b - n0, 256));
   const uint32_t lds0 = lds_addr_of(smem);
 
-  const uint64_t step_a = uniform64(g.a.rows * 128), step_b = uniform64(g.b.rows * 128);
-  uint64_t code_a = uniform64((uint64_t)(g.a.codes + (kb0 * g.a.rows + m0) * 128));
-  uint64_t code_b = uniform64((uint64_t)(g.b.codes + (kb0 * g.b.rows + n0) * 128));
+  const uint64_t step_a = uniform64(g.a.rows * kHalf), step_b = uniform64(g.b.rows * kHalf);
+  uint64_t code_a = uniform64((uint64_t)(g.a.codes + (2 * kb0 * g.a.rows + m0) * kHalf));
+  uint64_t code_b = uniform64((uint64_t)(g.b.codes + (2 * kb0 * g.b.rows + n0) * kHalf));
   // the scales that this wave loads: even waves A's, odd ones B's
-  uint64_t scale = uniform64((uint64_t)(wave & 1 ? g.b.scales + kb0 * sb + n0 : g.a.scales + kb0 * sa + m0));
-  const uint64_t step_s = uniform64(wave & 1 ? sb : sa);
+  uint64_t scale = uniform64((uint64_t)(wave & 1 ? g.b.scales + kb0 * srows_b + n0 : g.a.scales + kb0 * srows_a + m0));
+  const uint64_t step_s = uniform64(wave & 1 ? srows_b : srows_a);
   const uint32_t bytes_s = wave & 1 ? scales_b : scales_a;
 
-  auto issue = [&](int s) {  // called for one stage after the other
+  // The loads of a stage, one at a time and one stage after the other: first, with
+  // a block's first stage, the scale bytes; then this wave's share of A's and B's rows.
+  rsrc_t pa, pb;
+  auto load = [&](int s, int u) {
     const uint32_t base = lds0 + (s & 3) * C::kStage;
-    const int half = (s & 1) * kHalf;
-    const rsrc_t pa = uniform_rsrc(code_a, bytes_a);
-    const rsrc_t pb = uniform_rsrc(code_b, bytes_b);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int b = wave * MI + i;
-      load_lds16_so(pa, base + b * 1024, voff, b * 2048 + half);
+    if (u == 0) {
+      pa = uniform_rsrc(code_a, bytes_a);
+      pb = uniform_rsrc(code_b, bytes_b);
     }
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int b = wave * NI + j;
-      load_lds16_so(pb, base + BM * kHalf + b * 1024, voff, b * 2048 + half);
+    if (u < MI) {
+      const int b = wave * MI + u;
+      load_lds16_so(pa, base + b * 1024, voff, b * 1024);
+    } else if (u < MI + NI) {
+      const int b = wave * NI + u - MI;
+      load_lds16_so(pb, base + BM * kHalf + b * 1024, voff, b * 1024);
     }
-    // every wave issues as many loads, so that it can wait for a count of them
-    load_lds4(uniform_rsrc(scale, bytes_s), base + (BM + BN) * kHalf + wave * 256, lane * 4);
-    if (half) {
+    if (u == MI + NI - 1) {
       code_a += step_a;
       code_b += step_b;
-      scale += step_s;
     }
+  };
+  auto load_scales = [&](int s) {
+    load_lds4(uniform_rsrc(scale, bytes_s), lds0 + (s & 3) * C::kStage + (BM + BN) * kHalf + wave * 256, lane * 4);
+    scale += step_s;
   };
 
   struct Frags {
     pw8_codes_t a[MI], b[NI];
-    int sa[MI], sb[NI];
   };
+  int sa[2][MI], sb[2][NI];  // scales of a block, and of the next one
   const int frow = lane & 31, fh = lane >> 5;
   const int sw = (frow >> 2) & 3;
   const int c0 = ((2 * fh) ^ sw) << 4, c1 = ((2 * fh + 1) ^ sw) << 4;
@@ -204,87 +208,135 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
     return v;
   };
-  auto read = [&](int s, Frags& f) {
+  // One fragment of stage s, in the order of use: A's first, all of B's, the rest of A's.
+  constexpr int kFrags = MI + NI;
+  auto read = [&](int s, int u, Frags& f) {
     const unsigned char* st = smem + (s & 3) * C::kStage;
-    const unsigned char* sc = st + (BM + BN) * kHalf;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int r = wm * MI * 32 + i * 32 + frow;
-      f.a[i] = fragment(st + r * kHalf);
-      f.sa[i] = sc[r];
+    if (u == 0 || u > NI) {
+      const int i = u ? u - NI : 0;
+      f.a[i] = fragment(st + (wm * MI * 32 + i * 32 + frow) * kHalf);
+    } else {
+      const int j = u - 1;
+      f.b[j] = fragment(st + (BM + wn * NI * 32 + j * 32 + frow) * kHalf);
     }
+  };
+  auto read_scales = [&](int s, int* na, int* nb) {
+    const unsigned char* sc = smem + (s & 3) * C::kStage + (BM + BN) * kHalf;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int r = wn * NI * 32 + j * 32 + frow;
-      f.b[j] = fragment(st + (BM + r) * kHalf);
-      f.sb[j] = sc[256 + r];
-    }
+    for (int i = 0; i < MI; ++i) na[i] = sc[wm * MI * 32 + i * 32 + frow];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) nb[j] = sc[256 + wn * NI * 32 + j * 32 + frow];
+  };
+  // every wave's loads for the next stage have landed, as each has waited for its own
+  auto meet = [&]() {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
   // the columns' operand first: a lane then holds 4 consecutive columns of a row
-  auto multiply = [&](const Frags& f) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        bf16x8_t wa[MI], wb[NI];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) wa[i] = pw8_wide(f.a[i], u, f.sa[i]);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) wb[j] = pw8_wide(f.b[j], u, f.sb[j]);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[j], f.a[i], acc[i][j], 0, 0, 0, f.sb[j], 0,
-                                                                    f.sa[i]);
+  auto multiply = [&](const Frags& f, int i, int j, const int* xa, const int* xb) {
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[j], f.a[i], acc[i][j], 0, 0, 0, xb[j], 0, xa[i]);
   };
-  constexpr int kReads = 3 * (MI + NI);
-  auto interleave = [&]() {
+  auto multiply_wide = [&](const Frags& f, const int* xa, const int* xb) {
 #pragma unroll
-    for (int u = 0; u < MI * NI; ++u) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                              // matrix instructions
-      __builtin_amdgcn_sched_group_barrier(0x100, (kReads + MI * NI - 1) / (MI * NI), 0);  // LDS reads
+    for (int u = 0; u < 4; ++u) {
+      bf16x8_t wa[MI], wb[NI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) wa[i] = pw8_wide(f.a[i], u, xa[i]);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) wb[j] = pw8_wide(f.b[j], u, xb[j]);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
     }
-  };
-  auto wait_stage = [&](int later) {  // how many stages may still be under way
-    if (later >= 3) wait_vm<3 * C::kLoads>();
-    else if (later == 2) wait_vm<2 * C::kLoads>();
-    else if (later == 1) wait_vm<C::kLoads>();
-    else wait_vm<0>();
   };
 
+  // Step s of a block's two (ODD): the products of stage s, from registers. Under
+  // them: wait until stage s + 1 has landed in all waves' LDS, read its fragments,
+  // and load stage s + 3 over stage s - 1, which every wave has used up. FULL:
+  // there are such stages; else that is looked at.
+  constexpr int kSlots = MI * NI, kAfter = kSlots > 4 ? 1 : 0;  // the products before the barrier
+  constexpr int kRoom = kSlots - kAfter;
   Frags f[2];
+  auto step = [&](int s, auto odd_, auto full_) {
+    constexpr bool ODD = decltype(odd_)::value, FULL = decltype(full_)::value;
+    const Frags& now = f[ODD];
+    Frags& next = f[!ODD];
+    const bool more = FULL || s + 1 < stages, ahead = FULL || s + 3 < stages;
+    if constexpr (sizeof(T) == 4) {
+      if (more) {
+        if (FULL || s + 2 < stages) wait_vm<C::kLoads + !ODD>();
+        else wait_vm<0>();
+        meet();
+        if (ODD) read_scales(s + 1, sa[1], sb[1]);
+        if (ahead) {
+          if (ODD) load_scales(s + 3);
 #pragma unroll
-  for (int s = 0; s < C::kRing; ++s)
-    if (s < stages) issue(s);
-  if (stages > 0) {
-    wait_stage(min(C::kRing, stages) - 1);
-    __syncthreads();
-    read(0, f[0]);
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): stage 0 is in registers
-  }
-  // one stage: wait for the next one, refill this one's place, read the next
-  // one's fragments under this one's products
-  auto step = [&](int s, const Frags& now, Frags& next) {
-    if (s + 1 < stages) {
-      wait_stage(min(s + C::kRing, stages) - 2 - s);
-      __syncthreads();
-      if (s + C::kRing < stages) issue(s + C::kRing);
-      read(s + 1, next);
+          for (int u = 0; u < kFrags; ++u) load(s + 3, u);
+        }
+#pragma unroll
+        for (int u = 0; u < kFrags; ++u) read(s + 1, u, next);
+      }
+      multiply_wide(now, sa[0], sb[0]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < kSlots; ++t) {
+        multiply(now, t / NI, t % NI, sa[0], sb[0]);
+        if (more) {
+          if (t == kAfter) {
+            // of stage s + 2, the only later one, its loads may still be under way
+            if (FULL || s + 2 < stages) wait_vm<C::kLoads + !ODD>();
+            else wait_vm<0>();
+            meet();
+            if (ODD) read_scales(s + 1, sa[1], sb[1]);
+            if (ODD && ahead) load_scales(s + 3);
+          }
+          if (t >= kAfter) {
+            const int r = t - kAfter;
+#pragma unroll
+            for (int u = r * kFrags / kRoom; u < (r + 1) * kFrags / kRoom; ++u) {
+              read(s + 1, u, next);
+              if (ahead) load(s + 3, u);
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    multiply(now);
-    if (sizeof(T) == 2) interleave();
-    __builtin_amdgcn_s_waitcnt(0xc07f);
+    if (ODD) {  // the next step is the next block's
+#pragma unroll
+      for (int i = 0; i < MI; ++i) sa[0][i] = sa[1][i];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) sb[0][j] = sb[1][j];
+    }
   };
-  for (int s = 0; s < stages; s += 2) {  // a block is two stages
-    step(s, f[0], f[1]);
-    step(s + 1, f[1], f[0]);
+  using Yes = std::integral_constant<bool, true>;
+  using No = std::integral_constant<bool, false>;
+
+  // three stages ahead; a block is two
+  load_scales(0);
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    if (s < stages) {
+      if (s == 2) load_scales(s);
+#pragma unroll
+      for (int u = 0; u < kFrags; ++u) load(s, u);
+    }
+  }
+  if (stages > 2) wait_vm<2 * C::kLoads + 1>();
+  else wait_vm<C::kLoads>();
+  meet();
+  read_scales(0, sa[0], sb[0]);
+#pragma unroll
+  for (int u = 0; u < kFrags; ++u) read(0, u, f[0]);
+  int s = 0;
+  for (; s + 4 < stages; s += 2) {
+    step(s, No(), Yes());
+    step(s + 1, Yes(), Yes());
+  }
+  for (; s < stages; s += 2) {
+    step(s, No(), No());
+    step(s + 1, Yes(), No());
   }
   __syncthreads();
 

@@ -6,12 +6,6 @@
 // by 2^-e is exact; e4m3's values keep 4 significant bits over 15 binades
 // whatever the scale.
 //
-// A matrix of codes over rows and a depth is stored by blocks of the depth:
-// codes [ceil(depth / 128)][rows][128], the last block filled up with zeros, and
-// scale bytes [ceil(depth / 128)][round_up(rows, 16)].  A product's tile of a
-// block is then one piece of memory, with 32-bit offsets inside it however large
-// the matrix is.
-//
 // One workgroup takes 128 x 128 values once and writes them in up to two forms:
 // the near form, whose depth runs along memory, and the far form, whose depth
 // runs across it (x for y, and x for dw).  What bounds it is memory: for bf16 in
@@ -178,7 +172,7 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
       c.x = pw8_codes4(pw8_scaled(v[i][0], inv), pw8_scaled(v[i][1], inv), pw8_scaled(v[i][2], inv), pw8_scaled(v[i][3], inv));
       c.y = pw8_codes4(pw8_scaled(v[i][4], inv), pw8_scaled(v[i][5], inv), pw8_scaled(v[i][6], inv), pw8_scaled(v[i][7], inv));
       if (l0 + i < a.lines) {
-        *(uint2*)(a.near_codes + ((int64_t)near_at * a.lines + l0 + i) * kTile + q * kRun) = c;
+        *(uint2*)(a.near_codes + pw8_code(near_at, q / 8, a.lines, l0 + i) + q % 8 * kRun) = c;
         if (q == 0) a.near_scales[(int64_t)near_at * pw8_scale_rows(a.lines) + l0 + i] = (uint8_t)byte;
       }
     }
@@ -201,14 +195,15 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
         a.far_scales[(int64_t)lines_at * pw8_scale_rows(a.near) + near0 + b] = (uint8_t)bytes[j];
     }
     __syncthreads();
-    unsigned char* dst = a.far_codes + ((int64_t)lines_at * a.near + near0) * kTile;
+    // 16-byte pieces in the order of memory: half, column, piece
 #pragma unroll
     for (int i = 0; i < kTile * kTile / 16 / kThreads; ++i) {
-      const int piece = i * kThreads + tid, b = piece >> 3, c = (piece & 7) * 2, o = b >> 3;
+      const int piece = i * kThreads + tid, half = piece / (4 * kTile), b = piece / 4 % kTile, o = b >> 3;
+      const int c = half * 8 + (piece & 3) * 2;
       if (near0 + b < a.near) {
         const uint2 lo = *(const uint2*)(turned + b * kTile + ((c ^ o) << 3));
         const uint2 hi = *(const uint2*)(turned + b * kTile + (((c + 1) ^ o) << 3));
-        *(uint4*)(dst + piece * 16) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        *(uint4*)(a.far_codes + pw8_code(lines_at, half, a.near, near0 + b) + (piece & 3) * 16) = make_uint4(lo.x, lo.y, hi.x, hi.y);
       }
     }
   }
