@@ -303,7 +303,7 @@ hipError_t launch_pw8_few(const Pw8FewArgs& a, int dtype, int cus, hipStream_t s
 // workspace: X twice, kMuonSquares matrices of the smaller side, partial sums of
 // squares and of products.  X has the smaller side first (m <= n), so it is a tall
 // matrix's transpose.  Sides are rounded up to 32 with zeros (mp, np), values are
-// pairs of fp16 in two planes.
+// pairs of fp16.
 constexpr int kMuonList = 48;      // matrices of a launch
 constexpr int kMuonPad = 32, kMuonSquares = 6, kMuonSums = 256;
 struct MuonItem {
@@ -350,9 +350,20 @@ inline int64_t muon_chunk(int64_t n) {
   const int64_t least = 4096, c = (n + kMuonSums - 1) / kMuonSums;
   return c <= least ? least : (c + 1023) / 1024 * 1024;
 }
+// A matrix whose step one workgroup does in LDS: 64 rows at most, and the bytes of X, two
+// squares and, for 32 rows, four waves' sums.
+constexpr int kMuonSmallSide = 64, kMuonSmallLds = 150 * 1024;
+inline int64_t muon_small_lds(int m, int n) {
+  return muon_x_bytes(m, n) + 2 * muon_square_bytes(m) + (m <= 32 ? 4 * 32 * 33 * 4 : 0);
+}
+struct MuonSmall {
+  int steps, lds;
+  float g, a, b, c, x, o;  // factors of sums: G; Q = a I + b G + c G^2; X; the update
+};
+hipError_t launch_muon_small(const MuonArgs& a, const MuonSmall& c, int p_dtype, int g_dtype, bool master, hipStream_t st);
 hipError_t launch_muon_momentum(const MuonArgs& a, uint32_t blocks, int g_dtype, hipStream_t st);
 hipError_t launch_muon_scale(const MuonArgs& a, uint32_t blocks, int g_dtype, hipStream_t st);
-// tile: 64 or 128; phases: 1 or 2 products in one launch
+// tile: 64, 128 or 256; phases: 1 or 2 products in one launch
 hipError_t launch_muon_square(const MuonArgs& a, uint32_t blocks, int tile, int phases, bool split, hipStream_t st);
 hipError_t launch_muon_join(const MuonArgs& a, uint32_t blocks, hipStream_t st);
 hipError_t launch_muon_apply(const MuonArgs& a, uint32_t blocks, int tile, bool last, int p_dtype, bool master,

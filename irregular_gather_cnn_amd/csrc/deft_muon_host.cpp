@@ -17,12 +17,6 @@ namespace {
 constexpr int64_t kMaxSide = 1 << 15, kMaxLong = 1 << 22, kMaxElems = (int64_t)1 << 32;
 constexpr int64_t kChunkBytes = (int64_t)2 << 30;          // workspace, but for single matrices that need more
 constexpr int kMaxSteps = 32;
-// Steps between two products with X: what is kept in fp32 goes with two, as near to
-// the formula's values as single steps are; three, for bf16 weights without
-// masters, take a quarter fewer operations where n = 9 m and are off by up to 8e-6
-// of the update instead of 1e-6, a hundredth of the weights' rounding.
-constexpr int kFusedF32 = 2, kFusedBf16 = 3;
-
 // Newton-Schulz coefficients: sigma -> a sigma + b sigma^3 + c sigma^5 takes
 // singular values of (0, 1] to 0.68 .. 1.21 in five steps where they were over 0.002.
 constexpr double kA = 3.4445, kB = -4.7750, kC = 2.0315;
@@ -51,23 +45,42 @@ struct Chunk {
   deft::MuonItem it[deft::kMuonList];
   int id[deft::kMuonList];
   int count = 0, next = 0;  // next: where in the list the following chunk starts
-  bool split = false;
+  int gram = 64, square = 64, apply = 64;  // tiles of the three kinds of product
+  bool split = false;       // Gram products in parts
+  bool small = false;       // every matrix fits one workgroup
+  int fused = 1;            // steps between two products with X
   int64_t bytes = 0;
 };
 
-// Tile of the products of squares: 128 where that gives every compute unit one.
-int square_tile(const Chunk& c, int cus) {
-  int64_t n = 0;
-  for (int i = 0; i < c.count; ++i) n += square_tiles(c.it[i].m, 128);
-  return n >= cus ? 128 : 64;
-}
 int64_t apply_tiles(int m, int n, int tile) {
   return ceil_div(deft::muon_pad(m), tile) * ceil_div(deft::muon_pad(n), tile);
 }
-int apply_tile(const Chunk& c, int cus) {
+template <typename F>
+int64_t sum(const Chunk& c, F of) {
   int64_t n = 0;
-  for (int i = 0; i < c.count; ++i) n += apply_tiles(c.it[i].m, c.it[i].n, 128);
-  return n >= cus / 2 ? 128 : 64;
+  for (int i = 0; i < c.count; ++i) n += of(c.it[i]);
+  return n;
+}
+void choose_tiles(Chunk& c, int cus) {
+  auto squares = [&](int t) { return sum(c, [&](const deft::MuonItem& i) { return square_tiles(i.m, t); }); };
+  auto applies = [&](int t) { return sum(c, [&](const deft::MuonItem& i) { return apply_tiles(i.m, i.n, t); }); };
+  // Large tiles read less from LDS for a product, small ones fill the units: 8 matrices
+  // of 256 x 2304 take 240 us with these, 281 with 64 in P X, 300 with 128 in squares, 4
+  // of 1024 x 9216 1715, 2325 and 1860 (64 in squares); 256 there 2176.
+  c.square = squares(128) >= cus / 2 ? 128 : 64;
+  c.apply = applies(256) >= cus ? 256 : applies(128) >= cus / 2 ? 128 : 64;
+  // these are split over n as well: 4 of 1024 x 9216 1715 us with 256, 1823 with 128
+  c.gram = squares(256) >= cus / 8 ? 256 : squares(128) >= cus / 8 ? 128 : 64;
+  // Two steps between products with X take 4 products of squares more and, of 3 m^2 n
+  // operations, one Gram product and one with X fewer than two single ones. Three at a
+  // time would take a quarter off where n = 9 m, but for some spectra the directions are
+  // off by 6 times as much as those of single steps in fp32, not by up to twice.
+  double wide = 0.0, square = 0.0;
+  for (int i = 0; i < c.count; ++i) {
+    wide += (double)c.it[i].m * c.it[i].m * c.it[i].n;
+    square += (double)c.it[i].m * c.it[i].m * c.it[i].m;
+  }
+  c.fused = wide > 2.0 * square ? 2 : 1;
 }
 
 // The next chunk of the list from `at` on; its items' shares start at `base`.
@@ -88,15 +101,21 @@ void next_chunk(const deft_muon_tensor* t, int count, int at, int cus, char* bas
     most += need;
     c.id[c.count++] = c.next;
   }
+  c.small = true;
+  for (int i = 0; i < c.count; ++i)
+    c.small &= c.it[i].m <= deft::kMuonSmallSide && deft::muon_small_lds(c.it[i].m, c.it[i].n) <= deft::kMuonSmallLds;
+  if (c.small) {  // no workspace
+    c.bytes = 0;
+    return;
+  }
   // the sums over n are split where their tiles leave compute units idle, into no
-  // fewer than 4 stages
-  const int tile = square_tile(c, cus);
-  int64_t tiles = 0;
-  for (int i = 0; i < c.count; ++i) tiles += square_tiles(c.it[i].m, tile);
-  const int64_t splits = tiles ? std::max<int64_t>(1, 2 * cus / tiles) : 1;
+  // fewer than 16 stages
+  choose_tiles(c, cus);
+  const int64_t tiles = sum(c, [&](const deft::MuonItem& i) { return square_tiles(i.m, c.gram); });
+  const int64_t splits = tiles ? std::max<int64_t>(1, (c.gram == 256 ? 1 : 2) * cus / tiles) : 1;
   c.split = false;
   for (int i = 0; i < c.count; ++i) {
-    c.it[i].splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, deft::muon_pad(c.it[i].n) / (4 * deft::kMuonPad)));
+    c.it[i].splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, deft::muon_pad(c.it[i].n) / 256));
     c.split |= c.it[i].splits > 1;
   }
   for (int i = 0; i < c.count; ++i) {
@@ -118,33 +137,30 @@ uint32_t lay(deft::MuonArgs& a, F of) {
 
 struct Launcher {
   deft::MuonArgs& a;
-  int tile, wide, p_dtype;
-  bool split, master;
+  const Chunk& c;
+  int p_dtype;
+  bool master;
   hipStream_t st;
   hipError_t e = hipSuccess;
 
   void gram(int x, int out) {
     if (e != hipSuccess) return;
     a.ph[0] = {x, x, out, -1, (float)(kSg / (kSx * kSx)), 0.f, 0.f};
-    const int t = tile;
-    const bool s = split;
-    const uint32_t n = lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, t) * (s ? i.splits : 1); });
-    e = deft::launch_muon_square(a, n, tile, 1, split, st);
-    if (e != hipSuccess || !split) return;
+    const uint32_t n = lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, c.gram) * (c.split ? i.splits : 1); });
+    e = deft::launch_muon_square(a, n, c.gram, 1, c.split, st);
+    if (e != hipSuccess || !c.split) return;
     e = deft::launch_muon_join(a, lay(a, [](const deft::MuonItem& i) { return square_tiles(i.m, 32); }), st);
   }
   void squares(int phases) {
     if (e != hipSuccess) return;
-    const int t = tile;
-    e = deft::launch_muon_square(a, lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, t); }), tile, phases,
-                                 false, st);
+    e = deft::launch_muon_square(a, lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, c.square); }), c.square,
+                                 phases, false, st);
   }
   void apply(int p, double scale, int x, int out, bool last) {
     if (e != hipSuccess) return;
     a.ph[0] = {p, x, out, -1, (float)(last ? 1.0 / (scale * kSx) : 1.0 / scale), 0.f, 0.f};
-    const int t = wide;
-    e = deft::launch_muon_apply(a, lay(a, [&](const deft::MuonItem& i) { return apply_tiles(i.m, i.n, t); }), wide, last,
-                                p_dtype, master, st);
+    e = deft::launch_muon_apply(a, lay(a, [&](const deft::MuonItem& i) { return apply_tiles(i.m, i.n, c.apply); }), c.apply,
+                                last, p_dtype, master, st);
   }
 
   // `steps` <= 3 of them on the X in buffer x; the result goes to the other one, or to the weights.
@@ -243,6 +259,21 @@ int deft_muon_step(const deft_muon_desc* d, const deft_muon_tensor* t, int count
       y.decay = x.weight_decay;
       y.scale = x.scale;
     }
+    if (c.small) {
+      deft::MuonSmall f;
+      f.steps = d->steps;
+      f.lds = 0;
+      for (int i = 0; i < c.count; ++i) f.lds = std::max<int>(f.lds, (int)deft::muon_small_lds(c.it[i].m, c.it[i].n));
+      f.g = (float)(kSg / (kSx * kSx));
+      f.a = (float)(kA * kSq);
+      f.b = (float)(kB * kSq / kSg);
+      f.c = (float)(kC * kSq / (kSg * kSg));
+      f.x = (float)(1.0 / kSq);
+      f.o = (float)(1.0 / (kSq * kSx));
+      const hipError_t e = deft::launch_muon_small(a, f, d->p_dtype, d->g_dtype, d->master != 0, st);
+      if (e != hipSuccess) return status_of(e);
+      continue;
+    }
     hipError_t e = deft::launch_muon_momentum(
         a, lay(a, [](const deft::MuonItem& i) {
           const int64_t n = (int64_t)i.m * i.n;
@@ -253,10 +284,9 @@ int deft_muon_step(const deft_muon_desc* d, const deft_muon_tensor* t, int count
           a, lay(a, [](const deft::MuonItem& i) { return ceil_div(deft::muon_pad(i.m), 64) * ceil_div(deft::muon_pad(i.n), 64); }),
           d->g_dtype, st);
     if (e != hipSuccess) return status_of(e);
-    Launcher l{a, square_tile(c, cus), apply_tile(c, cus), d->p_dtype, c.split, d->master != 0, st};
+    Launcher l{a, c, d->p_dtype, d->master != 0, st};
     // as few parts as there may be, the larger ones first
-    const int most = d->p_dtype == DEFT_BF16 && !d->master ? kFusedBf16 : kFusedF32;
-    int parts = (d->steps + most - 1) / most, left = d->steps, x = 0;
+    int parts = (d->steps + c.fused - 1) / c.fused, left = d->steps, x = 0;
     for (; parts > 0; --parts) {
       const int k = (left + parts - 1) / parts;
       l.fused(k, x, parts == 1);

@@ -64,7 +64,7 @@ FAKE = 0x10000
 
 def step_call(count=1, control=None, schedule=None, ws=FAKE, ws_bytes=1 << 40, desc=None, null=(), **tensor):
     d = dict(p_dtype=0, g_dtype=0, master=0, nesterov=1, steps=5, lr=0.02, momentum=0.95, eps=1e-7)
-    t = dict(p=FAKE, g=FAKE, m=FAKE, master=None, rows=8, cols=24, weight_decay=0.0, scale=1.0)
+    t = dict(p=FAKE, g=FAKE, m=FAKE, master=None, rows=80, cols=240, weight_decay=0.0, scale=1.0)
     d.update(desc or {})
     t.update(tensor)
     d, t = L.deft_muon_desc(**d), (L.deft_muon_tensor * 1)(L.deft_muon_tensor(**t))
@@ -110,7 +110,9 @@ def test_workspace_bytes():
     assert need((256, 2304)) >= 4 * (2 * 256 * 2304 + 6 * 256 * 256)
     assert need((256, 2304)) == need((2304, 256))
     # a long list reuses what a launch's matrices need
-    assert need(*[(64, 64)] * 96) == need(*[(64, 64)] * 48)
+    assert need(*[(65, 65)] * 96) == need(*[(65, 65)] * 48) > 0
+    # matrices that fit one workgroup's memory need none, where all do
+    assert need((64, 64), (18, 144), (900, 3)) == 0 and need((64, 64), (65, 65)) > 0 and need((2, 2000)) > 0
 
 
 def test_python_class_refuses():
@@ -193,6 +195,7 @@ def check_direction(us, steps=5, eps=1e-7):
         assert off <= bound
 
 
+LARGE = (70, 90)  # with it in a list, no matrix takes the launch for small ones
 SHAPES = [(1, 1), (1, 7), (9, 1), (5, 3), (16, 144), (18, 144), (31, 33), (64, 64), (65, 32), (130, 70), (128, 129), (300, 1000),
           (1000, 300), (18, 2304), (256, 2304), (513, 513), (33, 5000)]
 
@@ -204,12 +207,28 @@ def test_direction_matches_the_oracle(shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [s for s in SHAPES if min(s) <= 64] + [(32, 960), (960, 32), (64, 352), (352, 64), (33, 31)])
+def test_small_matrices_among_large_ones(shape):
+    check_direction([rand(shape, 1), rand(LARGE, 2), rand(shape, 3)])
+    check_direction([rand(shape, 4), rand(shape, 5)])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shapes", [[(1024, 1100), (600, 2300), (1500, 700)], [(2100, 2049)], [(300, 5000)] * 9,
+                                    [(40, 60000), (60000, 33)]])
+def test_large_tiles(shapes):
+    check_direction([rand(s, 6 + k) for k, s in enumerate(shapes)])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 7, 10, 32])
 def test_any_number_of_steps(steps):
     # from 6 steps on an error's part that grows in all of them leaves the bound no meaning: the steps come to
     # rest between 0.68 and 1.21, which is checked instead
     us = [rand((40, 100), 2), rand((130, 70), 3)]
     if steps < 6:
+        check_direction(us[:1], steps)
         return check_direction(us, steps)
     for u, x in zip(us, direction(us, steps)):
         s = torch.linalg.svdvals(x.double().cpu())
@@ -230,7 +249,7 @@ def spectra(m, n):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["normal", "strong", "decades", "one"])
-@pytest.mark.parametrize("m,n", [(64, 64), (256, 700), (200, 200)])
+@pytest.mark.parametrize("m,n", [(64, 64), (64, 300), (256, 700), (200, 200)])
 def test_directions_are_as_near_as_steps_in_fp32(m, n, name):
     """Each step's products in fp32 torch, on the CPU, are the measure: no more than 4 times as far."""
     u = spectra(m, n)[name]
@@ -262,12 +281,14 @@ def test_sizes_of_directions():
 
 @pytest.mark.gpu
 def test_a_matrix_that_is_not_finite_stays_alone():
-    us = [rand((40, 90), 13), rand((100, 30), 14), rand((7, 7), 15)]
-    want = direction(us)
-    for bad in (math.nan, math.inf, -math.inf):
-        us[1][50, 3] = bad
-        got = direction_with_states(us)
-        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and torch.isnan(got[1]).all()
+    for extra in ([], [rand(LARGE, 16)]):
+        us = [rand((40, 90), 13), rand((100, 30), 14), rand((7, 7), 15)] + extra
+        want = direction(us)
+        for bad in (math.nan, math.inf, -math.inf):
+            us[1][50, 3] = bad
+            got = direction_with_states(us)
+            assert torch.isnan(got[1]).all()
+            assert all(torch.equal(got[k], want[k]) for k in range(len(us)) if k != 1)
 
 
 def direction_with_states(us):
@@ -286,14 +307,15 @@ def training(p_type, g_type, master, shapes, seed=20):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("small", [True, False])
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("clip", [True, False])
 @pytest.mark.parametrize("p_type,g_type,master", [("f32", "f32", False), ("f32", "bf16", False), ("bf16", "bf16", False),
                                                   ("bf16", "bf16", True), ("bf16", "f32", True)])
-def test_momentum_and_weights_bit_for_bit(p_type, g_type, master, clip, nesterov):
+def test_momentum_and_weights_bit_for_bit(p_type, g_type, master, clip, nesterov, small):
     """The direction of a step from zero weights gives the same bits, so the weights are compared with the
     formula on it."""
-    shapes = [(16, 4, 3, 3), (90, 30), (33, 70), (5, 5), (2, 2000)]
+    shapes = [(16, 4, 3, 3), (90, 30), (33, 70), (5, 5), (2, 200 if small else 2000)]
     p, g, m, masters = training(p_type, g_type, master, shapes)
     decay = [0.0, 0.1, 0.01, 0.3, 0.0]
     print("muon", p_type, g_type, master, clip, nesterov, flush=True)
@@ -323,13 +345,16 @@ def test_long_lists_take_several_launches():
     us = [rand(s, 200 + k) for k, s in enumerate(shapes)]
     got = direction(us)
     for k in (0, 46, 47, 48, 49, 95, 96, 97, 100, 103):
-        assert torch.equal(got[k], direction([us[k]])[0]) or float((got[k] - direction([us[k]])[0]).norm()) < 1e-4
+        assert torch.equal(got[k], direction([us[k]])[0])
     check_direction(us[:101:10] + us[103:])
+    us[60] = rand(LARGE, 500)  # the second launch's matrices are not all small, then
+    check_direction(us[:101] + us[103:])
 
 
 @pytest.mark.gpu
-def test_gradients_that_are_not_finite_skip_the_step():
-    p, g, m, masters = training("bf16", "bf16", True, [(40, 50), (200, 20)])
+@pytest.mark.parametrize("small", [True, False])
+def test_gradients_that_are_not_finite_skip_the_step(small):
+    p, g, m, masters = training("bf16", "bf16", True, [(40, 50), (200, 20)] + ([] if small else [LARGE]))
     opt = Muon(p, g, masters=masters, states=m)
     before = [t.clone() for t in p + m + masters]
     g[1][3, 3] = math.inf
@@ -372,8 +397,8 @@ def test_schedule_on_the_device_and_lr():
 
 
 @pytest.mark.gpu
-def test_captured_step_replays_like_eager_steps():
-    shapes = [(16, 4, 3, 3), (200, 90), (64, 1000)]
+@pytest.mark.parametrize("shapes", [[(16, 4, 3, 3), (200, 90), (64, 1000)], [(16, 4, 3, 3), (5, 70)]])
+def test_captured_step_replays_like_eager_steps(shapes):
     p, g, m, masters = training("bf16", "bf16", True, shapes)
     q = [[t.clone() for t in part] for part in (p, m, masters)]
     lr = torch.tensor([0.02], dtype=torch.float64, device="cuda")
@@ -416,9 +441,9 @@ def test_runs_on_the_current_stream_and_on_rebound_gradients():
 
 
 @pytest.mark.gpu
-def test_memory_behind_the_tensors_stays():
-    shapes = [(17, 45), (45, 17), (130, 3)]
-    flat = torch.full((3, 4096), 7.0, device="cuda")
+@pytest.mark.parametrize("shapes", [[(17, 45), (45, 17), (130, 3)], [(17, 45), (45, 17), (130, 3), (67, 71)]])
+def test_memory_behind_the_tensors_stays(shapes):
+    flat = torch.full((4, 8192), 7.0, device="cuda")
     for dtype in TYPES.values():
         base, moms = flat.to(dtype, copy=True), flat.clone()
         p = [base[k, :r * c].view(r, c) for k, (r, c) in enumerate(shapes)]
