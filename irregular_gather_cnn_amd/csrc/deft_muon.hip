@@ -760,7 +760,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BT == 256 ?
 // by one, the weights.  X lies in LDS in its panels, so a step is a product over n
 // for G (32 rows: the waves share n and add up; 64: a wave for each 32 x 32 block), a
 // small one for Q and one that replaces X's columns, each by one wave.  22 launches
-// of 4 us become one: [16][144] and [18][144] take 15 us where they took 90.
+// of 4 us become one: [16][144] and [18][144] take 23 us where they took 90, 2.6 for
+// each step and the rest for the launch, the loads and the stores.
 constexpr int kSmallThreads = 256;
 
 // A run's place in a matrix of panels in LDS: 16-byte pieces, high 0 and 1, low 2 and 3.
@@ -820,13 +821,13 @@ struct Sums3 {
   __device__ __forceinline__ f32x16_t all() const { return s[0] + (s[1] + s[2]); }
 };
 
-template <typename T, typename G, bool MASTER>
-__global__ __launch_bounds__(kSmallThreads) void k_muon_small(const MuonArgs a, const MuonSmall c) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ double part[4];
+// X has 32 * blocks rows.
+template <typename T, typename G, bool MASTER, int blocks>
+__device__ __forceinline__ void small_step(unsigned char* smem, double* part, const MuonArgs& a, const MuonSmall& c) {
   const MuonItem& t = a.it[blockIdx.x];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int m = t.m, n = t.n, mp = (int)muon_pad(m), np = (int)muon_pad(n);
+  constexpr int mp = 32 * blocks;
+  const int m = t.m, n = t.n, np = (int)muon_pad(n);
   unsigned char* x = smem;
   unsigned char* g = x + 4 * mp * np;
   unsigned char* q = g + 4 * mp * mp;
@@ -879,7 +880,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_muon_small(const MuonArgs a, 
   }
   __syncthreads();
 
-  const int blocks = mp / 32, bi = wave / blocks % blocks * 32, bj = wave % blocks * 32;  // this wave's block of a square
+  const int bi = wave / blocks % blocks * 32, bj = wave % blocks * 32;  // this wave's block of a square
   const int row = lane & 31, fh = lane >> 5;
   const double lr = a.schedule ? a.schedule[0] : a.lr;
   const float keep = (float)(1.0 - lr * t.decay), rate = (float)(lr * t.scale);
@@ -919,6 +920,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_muon_small(const MuonArgs a, 
     // Q = a I + b G + c G^2
     if (wave < blocks * blocks) {
       acc.clear();
+#pragma unroll
       for (int k = 0; k < mp / 16; ++k)
         acc.add(small_rows(g, mp, bi, k, 0, lane), small_rows(g, mp, bi, k, 1, lane), small_rows(g, mp, bj, k, 0, lane),
                 small_rows(g, mp, bj, k, 1, lane));
@@ -940,19 +942,18 @@ __global__ __launch_bounds__(kSmallThreads) void k_muon_small(const MuonArgs a, 
     // X <- Q X, or the weights
     const bool last = step + 1 == c.steps;
     for (int tile = wave; tile < np / 32; tile += 4) {
-      f32x16_t s[2];
+      f32x16_t s[blocks];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        if (b < blocks) {
+      for (int b = 0; b < blocks; ++b) {
           acc.clear();
+#pragma unroll
           for (int k = 0; k < mp / 16; ++k)
             acc.add(small_rows(q, mp, b * 32, k, 0, lane), small_rows(q, mp, b * 32, k, 1, lane),
                     small_columns(x, mp, k * 16, tile * 32, 0, lane), small_columns(x, mp, k * 16, tile * 32, 1, lane));
           s[b] = acc.all();
         }
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        if (b < blocks) {
+      for (int b = 0; b < blocks; ++b) {
           const int i = b * 32 + row, j0 = tile * 32 + 4 * fh;
           if (!last) {
 #pragma unroll
@@ -982,6 +983,14 @@ __global__ __launch_bounds__(kSmallThreads) void k_muon_small(const MuonArgs a, 
     }
     __syncthreads();
   }
+}
+
+template <typename T, typename G, bool MASTER>
+__global__ __launch_bounds__(kSmallThreads) void k_muon_small(const MuonArgs a, const MuonSmall c) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ double part[4];
+  if (a.it[blockIdx.x].m <= 32) small_step<T, G, MASTER, 1>(smem, part, a, c);
+  else small_step<T, G, MASTER, 2>(smem, part, a, c);
 }
 
 template <typename K>

@@ -23,6 +23,36 @@ __device__ __forceinline__ uint32_t pw8_finite_bits(float v) {
   return b < 0x7f800000u ? b : 0u;
 }
 __device__ __forceinline__ uint32_t pw8_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// v of the lane whose number within its 16 is greater by N, cyclically.
+template <int N> __device__ __forceinline__ uint32_t turn16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xf, 0xf, false);
+}
+// The greatest among 16 lanes, and among the lanes of the same number in each 16.
+__device__ __forceinline__ uint32_t max_of_16(uint32_t v) {
+  v = pw8_max(v, turn16<8>(v));
+  v = pw8_max(v, turn16<4>(v));
+  v = pw8_max(v, turn16<2>(v));
+  return pw8_max(v, turn16<1>(v));
+}
+__device__ __forceinline__ uint32_t max_across_16(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = pw8_max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return pw8_max(b[0], b[1]);
+}
+// Sums likewise, in an order that is the same for all lanes.
+__device__ __forceinline__ float sum_of_16(float v) {
+  v += __uint_as_float(turn16<8>(__float_as_uint(v)));
+  v += __uint_as_float(turn16<4>(__float_as_uint(v)));
+  v += __uint_as_float(turn16<2>(__float_as_uint(v)));
+  return v + __uint_as_float(turn16<1>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float sum_across_16(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
 // e + 127 of a block whose largest value has these bits.
 __device__ __forceinline__ int pw8_scale_byte(uint32_t most) {
   const int e = (int)(most >> 23) - 8 + ((most & 0x7fffffu) > 0x600000u);  // 448 = 1.75 * 2^8

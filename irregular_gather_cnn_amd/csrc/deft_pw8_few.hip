@@ -106,9 +106,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_pw8_few(const Pw8FewArgs a) {
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) m = pw8_max(m, pw8_finite_bits(v[j]));
-        m = pw8_max(m, __shfl_xor(m, 16));
-        m = pw8_max(m, __shfl_xor(m, 32));
-        const int byte = pw8_scale_byte(m);
+        const int byte = pw8_scale_byte(max_across_16(m));
         const float inv = pw8_inverse_scale(byte);
         pw8_codes_t q;
 #pragma unroll

@@ -62,43 +62,43 @@ __device__ __forceinline__ void store_run(float* p, const float* f) {
   *(word4*)(p + 4) = b;
 }
 
-// Where output (i, j .. j + 7) goes, with its bias.  positions: j runs over the
-// positions of all images, i over channels (channels first); else row-major.
+// Where a lane's runs of 8 columns go: column j of row 0, and on from row to row.
+// positions: columns run over the positions of all images, rows over channels
+// (channels first); else row-major.  A run that passes the last column or an
+// image's end goes value by value.
 template <typename T>
-__device__ __forceinline__ void put_run(const Pw8Out& o, T* out, int64_t i, int64_t j, float* f) {
-  const int64_t left = o.cols - j;
-  if (o.bias) {
-    if (o.positions) {
-      const float b = Elem<T>::to_f32(((const T*)o.bias)[i]);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) f[u] += b;
-    } else {
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (u < left) f[u] += Elem<T>::to_f32(((const T*)o.bias)[j + u]);
+struct Runs {
+  T* p;
+  int64_t j, pitch, left, room, rows, positions;
+  __device__ __forceinline__ Runs(const Pw8Out& o, int64_t j_) : j(j_), rows(o.rows), positions(o.positions) {
+    left = room = o.cols - j;
+    pitch = o.cols;
+    int64_t at = j;
+    if (positions) {
+      const int64_t image = (uint32_t)j / (uint32_t)positions, pos = j - image * positions;
+      at = image * rows * positions + pos;
+      pitch = positions;
+      if (positions - pos < room) room = positions - pos;
     }
+    p = (T*)o.p + at;
   }
-  int64_t at = i * o.cols + j, room = left;
-  if (o.positions) {
-    const int64_t image = (uint32_t)j / (uint32_t)o.positions, pos = j - image * o.positions;
-    at = (image * o.rows + i) * o.positions + pos;
-    if (o.positions - pos < room) room = o.positions - pos;
-  }
-  if (room >= 8) {
-    store_run(out + at, f);
-    return;
-  }
+  __device__ __forceinline__ void put(int64_t i, const float* f) const {
+    if (room >= 8) {
+      store_run(p + i * pitch, f);
+      return;
+    }
 #pragma unroll
-  for (int u = 0; u < 8; ++u)
-    if (u < left) {
-      int64_t p = at + u;
-      if (o.positions) {
-        const int64_t image = (uint32_t)(j + u) / (uint32_t)o.positions;
-        p = (image * o.rows + i) * o.positions + (j + u - image * o.positions);
+    for (int u = 0; u < 8; ++u)
+      if (u < left) {
+        int64_t at = i * pitch + u;
+        if (positions && u >= room) {  // the next image, or, of fewer than 8 positions, a later one
+          const int64_t next = positions >= 8 ? 1 : (uint32_t)(u - (int)room) / (uint32_t)positions + 1;
+          at += next * (rows - 1) * positions;
+        }
+        p[at] = Elem<T>::from_f32(f[u]);
       }
-      out[p] = Elem<T>::from_f32(f[u]);
-    }
-}
+  }
+};
 
 // One workgroup of 2 x 2 waves computes BM x BN outputs over a range of blocks.
 //
@@ -257,6 +257,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   // there are such stages; else that is looked at.
   constexpr int kSlots = MI * NI, kAfter = kSlots > 4 ? 1 : 0;  // the products before the barrier
   constexpr int kRoom = kSlots - kAfter;
+  // the biases of this lane's outputs, asked for before the products
+  constexpr int kRuns = NI * 32 / 8, kRowsAt = 64 / kRuns, kPasses = 32 / kRowsAt;
+  const int64_t mw = m0 + wm * MI * 32, nw = n0 + wn * NI * 32;
+  const int erow = lane / kRuns, ecol = (lane % kRuns) * 8;
+  float bias[MI * kPasses > 8 ? MI * kPasses : 8];
+  if (!PARTIAL) {
+#pragma unroll
+    for (int u = 0; u < (MI * kPasses > 8 ? MI * kPasses : 8); ++u) {
+      // positions: the rows' (every kRowsAt-th); else the columns'
+      const int64_t at = g.out.positions ? mw + u * kRowsAt + erow : nw + ecol + u;
+      const bool in = g.out.bias && (g.out.positions ? u < MI * kPasses && at < g.out.rows : u < 8 && at < g.out.cols);
+      bias[u] = in ? Elem<T>::to_f32(((const T*)g.out.bias)[at]) : 0.f;
+    }
+  }
+
   Frags f[2];
   auto step = [&](int s, auto odd_, auto full_) {
     constexpr bool ODD = decltype(odd_)::value, FULL = decltype(full_)::value;
@@ -343,8 +358,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   // out through LDS, 32 rows of the wave at a time, so that lanes next to each
   // other store next to each other
   unsigned char* mine = smem + wave * 32 * C::kEpiPitch;
-  constexpr int kRuns = NI * 32 / 8, kRowsAt = 64 / kRuns;
-  const int64_t mw = m0 + wm * MI * 32, nw = n0 + wn * NI * 32;
+  const int64_t col = nw + ecol;
+  const Runs<T> runs(g.out, col);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -356,22 +371,22 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
       }
     __builtin_amdgcn_s_waitcnt(0xc07f);
 #pragma unroll
-    for (int u = 0; u < 32 / kRowsAt; ++u) {
-      const int r = u * kRowsAt + lane / kRuns, c = (lane % kRuns) * 8;
-      const int64_t row = mw + i * 32 + r, col = nw + c;
+    for (int u = 0; u < kPasses; ++u) {
+      const int r = u * kRowsAt + erow;
+      const int64_t row = mw + i * 32 + r;
       if (row < g.out.rows && col < g.out.cols) {
-        float v[8];
-        const float4 lo = *(const float4*)(mine + r * C::kEpiPitch + c * 4);
-        const float4 hi = *(const float4*)(mine + r * C::kEpiPitch + c * 4 + 16);
-        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        const float4 lo = *(const float4*)(mine + r * C::kEpiPitch + ecol * 4);
+        const float4 hi = *(const float4*)(mine + r * C::kEpiPitch + ecol * 4 + 16);
         if (PARTIAL) {
           // rows of whole runs: cols is rounded up to 8
           float* p = g.part + ((int64_t)split * g.out.rows + row) * g.part_cols + col;
           *(float4*)p = lo;
           *(float4*)(p + 4) = hi;
         } else {
-          put_run<T>(g.out, (T*)g.out.p, row, col, v);
+          float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += g.out.positions ? bias[i * kPasses + u] : bias[e];
+          runs.put(row, v);
         }
       }
     }
@@ -410,7 +425,12 @@ __global__ __launch_bounds__(256) void k_pw8_join(const Pw8Out o, const float* p
     v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
     v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
   }
-  put_run<T>(o, (T*)o.p, i, j, v);
+  if (o.bias) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (o.positions || j + u < o.cols) v[u] += Elem<T>::to_f32(((const T*)o.bias)[o.positions ? i : j + u]);
+  }
+  Runs<T>(o, j).put(i, v);
 }
 
 template <typename T, int BM, int BN>

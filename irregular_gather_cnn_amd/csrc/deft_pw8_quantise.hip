@@ -25,23 +25,49 @@ constexpr int kAcross = kTile / kRun;              // threads along a line
 constexpr int kLines = kTile * kAcross / kThreads; // lines of a thread, in sequence
 static_assert(kLines == 8, "a thread holds 8 x 8 values");
 
-// 8 values from any element address.
-__device__ __forceinline__ void load_run(const bf16_t* p, float* f) {
+// 8 consecutive values of a line as they lie in memory, from any element address: half
+// the registers of their fp32 values in bf16, which lets four workgroups of 256 threads
+// share a unit instead of three.
+template <typename T> struct Run8;
+template <> struct Run8<bf16_t> {
   typedef uint32_t word4 __attribute__((ext_vector_type(4), aligned(2)));
-  const word4 w = *(const word4*)p;
-  unpack8(make_uint4(w.x, w.y, w.z, w.w), f);
-}
-__device__ __forceinline__ void load_run(const float* p, float* f) {
-  typedef float word4 __attribute__((ext_vector_type(4), aligned(4)));
-  const word4 a = *(const word4*)p, b = *(const word4*)(p + 4);
+  word4 w;
+  __device__ __forceinline__ void clear() { w = word4{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const bf16_t* p) { w = *(const word4*)p; }
+  __device__ __forceinline__ void set(const bf16_t* v) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) { f[j] = a[j]; f[4 + j] = b[j]; }
-}
+    for (int j = 0; j < 4; ++j) w[j] = v[2 * j] | (uint32_t)v[2 * j + 1] << 16;
+  }
+  // Between two passes over the values: the compiler would carry them from one to the
+  // other unpacked.
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t q = w[j];
+      asm volatile("" : "+v"(q));
+      w[j] = q;
+    }
+  }
+  __device__ __forceinline__ float get(int j) const { return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]); }
+};
+template <> struct Run8<float> {
+  typedef float word4 __attribute__((ext_vector_type(4), aligned(4)));
+  word4 w[2];
+  __device__ __forceinline__ void clear() { w[0] = w[1] = word4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ void load(const float* p) { w[0] = *(const word4*)p; w[1] = *(const word4*)(p + 4); }
+  __device__ __forceinline__ void set(const float* v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j >> 2][j & 3] = v[j];
+  }
+  __device__ __forceinline__ void keep() {}
+  __device__ __forceinline__ float get(int j) const { return w[j >> 2][j & 3]; }
+};
 
 // FAR: the far form is written, too (or alone).  TILE: one scale for the whole
 // tile.
 template <typename T, bool FAR, bool TILE>
-__global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs a) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 4 && FAR ? 3 : 4))) void k_pw8_quantise(const Pw8QuantiseArgs a,
+                                                                                                    const FastDiv by_positions) {
   // the waves' maxima of the 128 columns, then their sums; the far form's codes
   __shared__ uint32_t most_of[4][kTile];
   __shared__ float sum_of[4][kTile];
@@ -53,44 +79,48 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
   // this thread: lines line0 + 8 t + i, values b0 .. b0 + 7 along each
   const int64_t l0 = line0 + t * kLines, b0 = near0 + q * kRun;
 
-  float v[kLines][kRun];
+  Run8<T> v[kLines];
   {
     // where a run starts: lines are rows or, channels first, channels whose
     // positions go from image to image
     int64_t at = b0, room = a.near - b0;  // values that lie in sequence
+    const int64_t image_pitch = a.positions * a.lines;
     if (a.positions) {
-      const int64_t image = b0 / a.positions, pos = b0 - image * a.positions;
-      at = image * a.positions * a.lines + pos;
+      const int64_t image = fdiv((int)b0, by_positions), pos = b0 - image * a.positions;
+      at = image * image_pitch + pos;
       if (a.positions - pos < room) room = a.positions - pos;
     }
-    const T* src = (const T*)a.src + at + l0 * a.pitch;
+    const T* src = (const T*)a.src + l0 * a.pitch;
     const bool whole = room >= kRun;
 #pragma unroll
     for (int i = 0; i < kLines; ++i) {
-#pragma unroll
-      for (int j = 0; j < kRun; ++j) v[i][j] = 0.f;
-      if (l0 + i < a.lines && whole) load_run(src + i * a.pitch, v[i]);
+      v[i].clear();
+      if (l0 + i < a.lines && whole) v[i].load(src + at + i * a.pitch);
     }
-    if (!whole && b0 < a.near) {
-      // a line's end, or the border of two images (positions of an image may be
-      // fewer than a run, then there are several)
-#pragma unroll 1
+    if (!whole && b0 < a.near && l0 < a.lines) {
+      // a line's end, or the border of two images: value by value, all at once; what lies
+      // outside is read from the run's first place
+      int64_t p[kRun];
+#pragma unroll
       for (int j = 0; j < kRun; ++j) {
-        const int64_t b = b0 + j;
-        if (b >= a.near) break;
-        int64_t p = b;
-        if (a.positions) {
-          const int64_t image = b / a.positions;
-          p = image * a.positions * a.lines + (b - image * a.positions);
-        }
-#pragma unroll
-        for (int i = 0; i < kLines; ++i)
-          if (l0 + i < a.lines) {
-            const float w = Elem<T>::to_f32(((const T*)a.src)[p + (l0 + i) * a.pitch]);
-#pragma unroll
-            for (int k = 0; k < kRun; ++k)
-              if (k == j) v[i][k] = w;
+        p[j] = at;
+        if (b0 + j < a.near) {
+          p[j] = b0 + j;
+          if (a.positions) {
+            const int64_t image = fdiv((int)(b0 + j), by_positions);
+            p[j] = image * image_pitch + (b0 + j - image * a.positions);
           }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kLines; ++i) {
+        const T* line = src + (l0 + i < a.lines ? i : 0) * a.pitch;
+        T w[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) w[j] = line[p[j]];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) w[j] = b0 + j < a.near && l0 + i < a.lines ? w[j] : T(0);
+        v[i].set(w);
       }
     }
   }
@@ -102,9 +132,8 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
       for (int i = 0; i < kLines; ++i) {
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) s += v[i][j];
-#pragma unroll
-        for (int d = 1; d < kAcross; d <<= 1) s += __shfl_xor(s, d);
+        for (int j = 0; j < kRun; ++j) s += v[i].get(j);
+        s = sum_of_16(s);
         if (q == 0 && l0 + i < a.lines) a.sums[(int64_t)near_at * a.lines + l0 + i] = s;
       }
     } else {
@@ -112,14 +141,18 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
       for (int j = 0; j < kRun; ++j) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kLines; ++i) s += v[i][j];
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
+        for (int i = 0; i < kLines; ++i) s += v[i].get(j);
+        s = sum_across_16(s);
         if ((tid & 63) < kAcross) sum_of[wave][q * kRun + j] = s;
       }
     }
   }
 
+  auto keep = [&]() {
+#pragma unroll
+    for (int i = 0; i < kLines; ++i) v[i].keep();
+  };
+  keep();
   uint32_t line_most[kLines], column_most[kRun];
 #pragma unroll
   for (int j = 0; j < kRun; ++j) column_most[j] = 0;
@@ -128,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const uint32_t b = pw8_finite_bits(v[i][j]);
+      const uint32_t b = pw8_finite_bits(v[i].get(j));
       m = pw8_max(m, b);
       column_most[j] = pw8_max(column_most[j], b);
     }
@@ -138,8 +171,7 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
     // over the wave's lines, then over the waves
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      column_most[j] = pw8_max(column_most[j], __shfl_xor(column_most[j], 16));
-      column_most[j] = pw8_max(column_most[j], __shfl_xor(column_most[j], 32));
+      column_most[j] = max_across_16(column_most[j]);
       if ((tid & 63) < kAcross) most_of[wave][q * kRun + j] = column_most[j];
     }
   }
@@ -152,31 +184,28 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
 #pragma unroll
     for (int j = 0; j < kRun; ++j)
       for (int w = 0; w < 4; ++w) m = pw8_max(m, most_of[w][q * kRun + j]);
-#pragma unroll
-    for (int d = 1; d < kAcross; d <<= 1) m = pw8_max(m, __shfl_xor(m, d));
-    tile_byte = pw8_scale_byte(m);
+    tile_byte = pw8_scale_byte(max_of_16(m));
   }
 
+  keep();
   if (a.near_codes) {
 #pragma unroll
     for (int i = 0; i < kLines; ++i) {
       int byte = tile_byte;
       if (!TILE) {
-        uint32_t m = line_most[i];
-#pragma unroll
-        for (int d = 1; d < kAcross; d <<= 1) m = pw8_max(m, __shfl_xor(m, d));
-        byte = pw8_scale_byte(m);
+        byte = pw8_scale_byte(max_of_16(line_most[i]));
       }
       const float inv = pw8_inverse_scale(byte);
       uint2 c;
-      c.x = pw8_codes4(pw8_scaled(v[i][0], inv), pw8_scaled(v[i][1], inv), pw8_scaled(v[i][2], inv), pw8_scaled(v[i][3], inv));
-      c.y = pw8_codes4(pw8_scaled(v[i][4], inv), pw8_scaled(v[i][5], inv), pw8_scaled(v[i][6], inv), pw8_scaled(v[i][7], inv));
+      c.x = pw8_codes4(pw8_scaled(v[i].get(0), inv), pw8_scaled(v[i].get(1), inv), pw8_scaled(v[i].get(2), inv), pw8_scaled(v[i].get(3), inv));
+      c.y = pw8_codes4(pw8_scaled(v[i].get(4), inv), pw8_scaled(v[i].get(5), inv), pw8_scaled(v[i].get(6), inv), pw8_scaled(v[i].get(7), inv));
       if (l0 + i < a.lines) {
         *(uint2*)(a.near_codes + pw8_code(near_at, q / 8, a.lines, l0 + i) + q % 8 * kRun) = c;
         if (q == 0) a.near_scales[(int64_t)near_at * pw8_scale_rows(a.lines) + l0 + i] = (uint8_t)byte;
       }
     }
   }
+  keep();
   if (FAR && a.far_codes) {
     int bytes[kRun];
 #pragma unroll
@@ -186,8 +215,8 @@ __global__ __launch_bounds__(kThreads) void k_pw8_quantise(const Pw8QuantiseArgs
                       : pw8_scale_byte(pw8_max(pw8_max(most_of[0][b], most_of[1][b]), pw8_max(most_of[2][b], most_of[3][b])));
       const float inv = pw8_inverse_scale(bytes[j]);
       uint2 c;
-      c.x = pw8_codes4(pw8_scaled(v[0][j], inv), pw8_scaled(v[1][j], inv), pw8_scaled(v[2][j], inv), pw8_scaled(v[3][j], inv));
-      c.y = pw8_codes4(pw8_scaled(v[4][j], inv), pw8_scaled(v[5][j], inv), pw8_scaled(v[6][j], inv), pw8_scaled(v[7][j], inv));
+      c.x = pw8_codes4(pw8_scaled(v[0].get(j), inv), pw8_scaled(v[1].get(j), inv), pw8_scaled(v[2].get(j), inv), pw8_scaled(v[3].get(j), inv));
+      c.y = pw8_codes4(pw8_scaled(v[4].get(j), inv), pw8_scaled(v[5].get(j), inv), pw8_scaled(v[6].get(j), inv), pw8_scaled(v[7].get(j), inv));
       // 8 lines of column b; columns of one j take the 8-byte places of a row of
       // the turned tile in different orders, so 16 threads write to 16 banks' pairs
       *(uint2*)(turned + b * kTile + ((t ^ q) << 3)) = c;
@@ -239,14 +268,15 @@ __global__ __launch_bounds__(256) void k_pw8_zero(uint16_t* p, size_t halves) {
 
 template <typename T>
 hipError_t quantise(const Pw8QuantiseArgs& a, uint32_t blocks, bool tile, hipStream_t st) {
+  const FastDiv by = make_fastdiv(a.positions ? (uint32_t)a.positions : 1u);
   if (tile && a.far_codes)
-    DEFT_LAUNCH("pw8_pack", (k_pw8_quantise<T, true, true>), dim3(blocks), dim3(kThreads), 0, st, a);
+    DEFT_LAUNCH("pw8_pack", (k_pw8_quantise<T, true, true>), dim3(blocks), dim3(kThreads), 0, st, a, by);
   else if (tile)
-    DEFT_LAUNCH("pw8_pack", (k_pw8_quantise<T, false, true>), dim3(blocks), dim3(kThreads), 0, st, a);
+    DEFT_LAUNCH("pw8_pack", (k_pw8_quantise<T, false, true>), dim3(blocks), dim3(kThreads), 0, st, a, by);
   else if (a.far_codes)
-    DEFT_LAUNCH("pw8_quantise", (k_pw8_quantise<T, true, false>), dim3(blocks), dim3(kThreads), 0, st, a);
+    DEFT_LAUNCH("pw8_quantise", (k_pw8_quantise<T, true, false>), dim3(blocks), dim3(kThreads), 0, st, a, by);
   else
-    DEFT_LAUNCH("pw8_quantise", (k_pw8_quantise<T, false, false>), dim3(blocks), dim3(kThreads), 0, st, a);
+    DEFT_LAUNCH("pw8_quantise", (k_pw8_quantise<T, false, false>), dim3(blocks), dim3(kThreads), 0, st, a, by);
   return hipGetLastError();
 }
 
