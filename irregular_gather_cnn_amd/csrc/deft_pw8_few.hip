@@ -29,6 +29,35 @@ template <> struct Run32<bf16_t> {
     const uint32_t q = w[j >> 3][(j >> 1) & 3];
     return j & 1 ? bf16_hi(q) : bf16_lo(q);
   }
+  // Bits of the greatest magnitude, as fp32; two at a time.
+  __device__ __forceinline__ uint32_t most() const {
+    typedef uint16_t half2_t __attribute__((ext_vector_type(2)));
+    half2_t m = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(half2_t, w[j >> 2][j & 3] & 0x7fff7fffu));
+    return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+  }
+  // Codes of finite values over 2^(byte - 127), byte > 0: one instruction for two.
+  __device__ __forceinline__ pw8_codes_t codes(int byte) const {
+    typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+    typedef short words_t __attribute__((ext_vector_type(2)));
+    const float scale = __uint_as_float((uint32_t)byte << 23);
+    pw8_codes_t c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t a = w[j >> 1][2 * (j & 1)], b = w[j >> 1][2 * (j & 1) + 1];
+      words_t q = {0, 0};
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(q, __builtin_bit_cast(pair_t, a), scale, false);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(q, __builtin_bit_cast(pair_t, b), scale, true);
+      c[j] = __builtin_bit_cast(int, q);
+    }
+    return c;
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = word4{0u, 0u, 0u, 0u};
+  }
 };
 template <> struct Run32<float> {
   typedef float word4 __attribute__((ext_vector_type(4), aligned(4)));
@@ -95,24 +124,39 @@ __global__ __launch_bounds__(64 * kWaves) void k_pw8_few(const Pw8FewArgs a) {
       const int kb = k0 + u * kWaves;
       if (kb < blocks) {
         const int c0 = kb * kPw8Block + h * 32;
-        float v[32];
-        if (live && step == 1 && c0 + 32 <= a.c_in) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = run[u].get(j);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = live && c0 + j < a.c_in ? Elem<T>::to_f32(x[(c0 + j) * step]) : 0.f;
-        }
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) m = pw8_max(m, pw8_finite_bits(v[j]));
-        const int byte = pw8_scale_byte(max_across_16(m));
-        const float inv = pw8_inverse_scale(byte);
+        int byte = 0;
         pw8_codes_t q;
+        bool done = false;
+        if constexpr (sizeof(T) == 2) {
+          // whole runs of finite values: a fifth of the operations of the general way
+          if (step == 1 && (kb + 1) * kPw8Block <= a.c_in) {
+            if (!live) run[u].clear();
+            const uint32_t m = max_across_16(run[u].most());
+            byte = pw8_scale_byte(m);
+            // codes of zeros are zeros over any power
+            done = !__any(m >= 0x7f800000u || (m != 0 && byte == 0));
+            if (done) q = run[u].codes(byte > 0 ? byte : 1);
+          }
+        }
+        if (!done) {
+          float v[32];
+          if (live && step == 1 && c0 + 32 <= a.c_in) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          q[j] = (int)pw8_codes4(pw8_scaled(v[4 * j], inv), pw8_scaled(v[4 * j + 1], inv), pw8_scaled(v[4 * j + 2], inv),
-                                 pw8_scaled(v[4 * j + 3], inv));
+            for (int j = 0; j < 32; ++j) v[j] = run[u].get(j);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = live && c0 + j < a.c_in ? Elem<T>::to_f32(x[(c0 + j) * step]) : 0.f;
+          }
+          uint32_t m = 0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) m = pw8_max(m, pw8_finite_bits(v[j]));
+          byte = pw8_scale_byte(max_across_16(m));
+          const float inv = pw8_inverse_scale(byte);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            q[j] = (int)pw8_codes4(pw8_scaled(v[4 * j], inv), pw8_scaled(v[4 * j + 1], inv), pw8_scaled(v[4 * j + 2], inv),
+                                   pw8_scaled(v[4 * j + 3], inv));
+        }
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
           pw8_codes_t w;
@@ -153,7 +197,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_pw8_few(const Pw8FewArgs a) {
 
 template <typename T>
 hipError_t few(const Pw8FewArgs& a, int cus, hipStream_t st) {
-  // 32 outputs a workgroup where that still leaves one for each compute unit
+  // 32 outputs a workgroup where that still leaves one for each compute unit: with 16 x is
+  // turned into codes twice as often (8 rows, 8192 to 8192: 21 us where they take 14.5,
+  // when that still took five times as many operations)
   constexpr int kAhead = sizeof(T) == 2 ? 4 : 1;
   if (a.w.rows >= (int64_t)32 * cus)
     DEFT_LAUNCH("pw8_few", (k_pw8_few<T, 2, kAhead>), dim3((uint32_t)((a.w.rows + 31) / 32)), dim3(64 * kWaves), 0, st, a);

@@ -277,7 +277,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
     constexpr bool ODD = decltype(odd_)::value, FULL = decltype(full_)::value;
     const Frags& now = f[ODD];
     Frags& next = f[!ODD];
-    const bool more = FULL || s + 1 < stages, ahead = FULL || s + 3 < stages;
+    const bool more = FULL || s + 1 < stages, ahead = FULL || (s + 3 < stages && stages > 4);
     if constexpr (sizeof(T) == 4) {
       if (more) {
         if (FULL || s + 2 < stages) wait_vm<C::kLoads + !ODD>();
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
         multiply(now, t / NI, t % NI, sa[0], sb[0]);
         if (more) {
           if (t == kAfter) {
-            // of stage s + 2, the only later one, its loads may still be under way
+            // of stage s + 2, the only later one (but in a depth of four), its loads may still be under way
             if (FULL || s + 2 < stages) wait_vm<C::kLoads + !ODD>();
             else wait_vm<0>();
             meet();
@@ -328,11 +328,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   using Yes = std::integral_constant<bool, true>;
   using No = std::integral_constant<bool, false>;
 
-  // three stages ahead; a block is two
+  // three stages ahead, or all four that a short depth has; a block is two
   load_scales(0);
 #pragma unroll
-  for (int s = 0; s < 3; ++s) {
-    if (s < stages) {
+  for (int s = 0; s < 4; ++s) {
+    if (s < 3 ? s < stages : stages == 4) {
       if (s == 2) load_scales(s);
 #pragma unroll
       for (int u = 0; u < kFrags; ++u) load(s, u);

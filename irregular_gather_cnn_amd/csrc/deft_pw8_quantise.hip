@@ -238,27 +238,33 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
   }
 }
 
-// db = the tiles' sums in their order.  64 channels a workgroup, 4 shares of the
-// tiles, fp64 beyond a tile.
+// db = the tiles' sums: 16 channels a workgroup, 16 shares of the tiles, fp64 beyond
+// a tile, in an order that does not change.
 template <typename T>
 __global__ __launch_bounds__(256) void k_pw8_bias(const float* sums, int64_t tiles, int c, T* db) {
-  __shared__ double part[4][64];
-  const int i = threadIdx.x & 63, share = threadIdx.x >> 6, ch = blockIdx.x * 64 + i;
+  __shared__ double part[16][16];
+  const int i = threadIdx.x & 15, share = threadIdx.x >> 4, ch = blockIdx.x * 16 + i;
   double s = 0.0;
   if (ch < c) {
     int64_t k = share;
-    for (; k + 28 < tiles; k += 32) {
+    for (; k + 112 < tiles; k += 128) {
       float f[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) f[u] = sums[(k + 4 * u) * c + ch];
+      for (int u = 0; u < 8; ++u) f[u] = sums[(k + 16 * u) * c + ch];
 #pragma unroll
       for (int u = 0; u < 8; ++u) s += (double)f[u];
     }
-    for (; k < tiles; k += 4) s += (double)sums[k * c + ch];
+#pragma unroll 8
+    for (; k < tiles; k += 16) s += (double)sums[k * c + ch];
   }
   part[share][i] = s;
   __syncthreads();
-  if (share == 0 && ch < c) db[ch] = Elem<T>::from_f32((float)((part[0][i] + part[1][i]) + (part[2][i] + part[3][i])));
+  if (share == 0 && ch < c) {
+    s = 0.0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) s += part[u][i];
+    db[ch] = Elem<T>::from_f32((float)s);
+  }
 }
 
 // Clears bytes (a multiple of 2) by a kernel: a memset does not belong in captured graphs.
@@ -293,7 +299,7 @@ hipError_t launch_pw8_zero(void* p, size_t bytes, hipStream_t st) {
 }
 
 hipError_t launch_pw8_bias(const float* sums, int64_t tiles, int c, void* db, int dtype, hipStream_t st) {
-  const dim3 grid((uint32_t)((c + 63) / 64));
+  const dim3 grid((uint32_t)((c + 15) / 16));
   if (dtype == DEFT_F32) DEFT_LAUNCH("pw8_bias", k_pw8_bias<float>, grid, dim3(256), 0, st, sums, tiles, c, (float*)db);
   else DEFT_LAUNCH("pw8_bias", k_pw8_bias<bf16_t>, grid, dim3(256), 0, st, sums, tiles, c, (bf16_t*)db);
   return hipGetLastError();
