@@ -18,8 +18,7 @@ LIB = os.path.join(PKG, "libdeft.so")
 SOURCES = ["deft_sample.hip", "deft_gemm.hip", "deft_gemm_dl.hip", "deft_igemm.hip", "deft_dwconv.hip",
            "deft_dwpw.hip", "deft_backward.hip", "deft_noalloc.hip", "deft_optim.hip", "deft_norm_fwd.hip",
            "deft_norm_bwd.hip", "deft_pw8_quantise.hip", "deft_pw8_gemm.hip", "deft_pw8_few.hip", "deft_muon.hip",
-           "deft_host.cpp",
-           "deft_train_host.cpp", "deft_pw8_host.cpp", "deft_muon_host.cpp"]
+           "deft_host.cpp", "deft_train_host.cpp", "deft_pw8_host.cpp", "deft_muon_host.cpp"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-Wall", "-Wno-unused-result",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

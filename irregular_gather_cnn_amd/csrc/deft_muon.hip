@@ -5,14 +5,12 @@
 //   X = u / max(|u|_F, eps);  per step  G = X X^T,  Q = a I + b G + c G^2,  X <- Q X
 //   p <- p (1 - lr wd) - lr s X
 // with the smaller side first.  All Q are polynomials of the first G, so they
-// commute, and up to three steps go without X:
-//   P <- Q P,  G <- Q G Q,   and X <- P X at the end.
-// For m x n that is one product over n for G and one for X instead of three
-// steps' six: 5 steps as 3 + 2 take 6 m^2 n + 14 m^3 operations (symmetric products
-// by halves) where they take 15 m^2 n + 5 m^3 one by one.  In a step G's error in
-// the directions of small singular values grows by a^2 = 12, so G is made from X
-// again after three; then results are as near to the formulas' values as those of
-// single steps in fp32 are (5 steps at once: 5 to 20 times farther).
+// commute, and two steps can go with one product with X:
+//   P = Q2 Q1,  where Q2 is made of G2 = Q1 G Q1,  and X <- P X.
+// For m x n matrices two single steps take 6 m^2 n + 2 m^3 operations (symmetric
+// products by halves), the two together 3 m^2 n + 5 m^3.  G2's error in the directions
+// of small singular values is G's times a^2 = 12; results stay within twice the error
+// of single steps in fp32 (three together: up to 6 times).
 //
 // Operands are pairs of fp16, hi + lo with 22 bits together, and a product is
 // three of the matrix instructions', hi hi + hi lo + lo hi, in fp32.  One fp16
@@ -283,7 +281,10 @@ __global__ __launch_bounds__(256) void k_muon_scale(const MuonArgs a) {
 // instructions, of which a stage has three for each 32 x 32 block.
 //
 // What bounds it is the tile: a wave of 64 x 64 reads as long from LDS as it
-// multiplies, one of 128 x 128 (BT 256, 256 accumulators) half as long.
+// multiplies, one of 128 x 128 (BT 256, 256 accumulators) half as long.  4 matrices of
+// 1024 x 9216: P X in 245 us and 314 with the weights (950 TFLOP/s of fp16, where the
+// instructions alone reach 1560 on random values), Gram products 135 (1070), squares
+// of 1024 by tiles of 128, which fill 144 units, 32 each.
 template <int BT>
 struct Tile {
   // Panels of a stage, and stages: small tiles take more of the depth between two

@@ -10,7 +10,7 @@
 // codes [ceil(depth / 128)][2][rows][64], the last block filled up with zeros, and
 // scale bytes [ceil(depth / 128)][round_up(rows, 16)].  What a stage of a product
 // reads is then one piece of memory, in whole lines (with 128 codes of a row in
-// sequence a stage read half lines: 8192^3 took 571 us where it takes 530), and
+// sequence a stage read half lines: 8192^3 took 608 us and then 554), and
 // offsets inside it fit 32 bits however large the matrix is.
 #pragma once
 #include "deft_device.h"

