@@ -275,6 +275,9 @@ class Muon:
             if p.dim() < 2:
                 raise ValueError("a param must have two dimensions or more, got %d" % p.dim())
         self.sizes = [p.numel() for p in self.params]
+        starts = [p.data_ptr() for p in self.params if p.numel()]
+        if len(set(starts)) < len(starts):
+            raise ValueError("a param is listed twice")
         self.shapes = [(p.shape[0], math.prod(p.shape[1:])) for p in self.params]
         self.grads = _Gradients(grads)
         if self.grads.sizes != self.sizes or self.grads.device != self.device:

@@ -134,6 +134,8 @@ def test_python_class_refuses():
     with pytest.raises(ValueError):
         muon(*make(shapes=((4, 6), (7,))))
     p, g, kw = make()
+    with pytest.raises(ValueError):
+        Muon([p[0], p[0]], [g[0], g[0]])
     for bad in (g[:1], [g[0], g[1][:2]], [g[0], torch.zeros(3, 2, 5)]):
         with pytest.raises((ValueError, TypeError)):
             Muon(p, bad)
@@ -457,3 +459,38 @@ def test_memory_behind_the_tensors_stays(shapes):
             assert (base[k, r * c:] == 7).all() and (moms[k, r * c:] == 7).all()
             assert torch.isfinite(p[k]).all() and not (p[k] == 7).all()
         assert (opt.ws[opt.ws_bytes:] == 0x7e).all()
+
+
+@pytest.mark.gpu
+def test_more_than_2_31_elements():
+    """The direction is P X0 with P a polynomial of X0 X0^T, which is summed up here in float64 by pieces."""
+    m, n = 520, (1 << 22) - 32
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of free memory")
+    print("muon", m, n, flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(70)
+    u = torch.randn((m, n), generator=gen, device="cuda")
+    p = torch.zeros_like(u)
+    opt = Muon([p], [u], lr=1.0, momentum=0.0, nesterov=False, weight_decay=0.0, adjust="none")
+    opt.step()
+    gram = torch.zeros((m, m), dtype=torch.float64, device="cuda")
+    for j in range(0, n, 1 << 18):
+        piece = u[:, j:j + (1 << 18)].double()
+        gram += piece @ piece.t()
+    norm = gram.diagonal().sum().sqrt()
+    gram /= norm * norm
+    poly, eye = torch.eye(m, dtype=torch.float64, device="cuda"), torch.eye(m, dtype=torch.float64, device="cuda")
+    sizes = 0.0
+    for _ in range(5):
+        sizes = O.STEEPEST * (sizes + float(gram.diagonal().sum().sqrt()))
+        q = O.A * eye + O.B * gram + O.C * gram @ gram
+        poly, gram = q @ poly, q @ gram @ q
+    bound = 32 * 2.0 ** -22 * (sizes + float(gram.diagonal().sum().sqrt()))
+    for j in (0, 1 << 20, n - 5000):
+        want = poly @ (u[:, j:j + 5000].double() / norm)
+        off = (-p[:, j:j + 5000].double() - want).norm()
+        # the columns are alike: an error's share of these is that of their number, 4 times that at most
+        assert float(off) <= 4 * bound * math.sqrt(5000 / n), j
+        assert float(want.norm()) > 100 * float(off)
+    del u, p, opt
+    torch.cuda.empty_cache()

@@ -440,3 +440,38 @@ def test_runs_on_the_current_stream():
         y, again = h.forward(late, packed, b)
     other.synchronize()
     assert torch.equal(y, want) and torch.equal(again[:saved.numel() // 2], saved[:saved.numel() // 2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_more_than_2_31_elements(layout):
+    """x of 2^31 + 2^25 elements; rows at its start, in its middle and at its end against the oracle."""
+    c_in, c_out, s = 8192, 40, (1 << 18) + 4099
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB of free memory")
+    print("pw8", c_in, s, c_out, layout, flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    shape = (1, s, c_in) if layout == "channels_last" else (1, c_in, s)
+    x = torch.randn(shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn((c_out, c_in), generator=gen, device="cuda").bfloat16()
+    dy = torch.randn((1, s, c_out) if layout == "channels_last" else (1, c_out, s), generator=gen, device="cuda").bfloat16()
+    h = Pointwise8(1, c_in, s, c_out, layout=layout, training=True)
+    packed = h.pack(w)
+    y, saved = h.forward(x, packed)
+    g = h.backward(saved, packed, dy)
+
+    def rows(t, at):
+        return (t[0, at:at + 100] if layout == "channels_last" else t[0, :, at:at + 100].t()).contiguous()
+
+    for at in (0, 1 << 17, (1 << 18) - 50, s - 100):
+        check_product("y", rows(y, at), O.forward(rows(x, at), w), c_in, "bf16")
+        want = O.backward(rows(x, at), w, rows(dy, at))["dx"]
+        check_product("dx", rows(g["dx"], at), want, c_out, "bf16")
+    # dw of the first and last channels
+    xr = x[0] if layout == "channels_last" else x[0].t()
+    dyr = dy[0] if layout == "channels_last" else dy[0].t()
+    for part in (slice(0, 20), slice(c_in - 20, c_in)):
+        want = O.product(O.coded(dyr.t()), O.coded(xr[:, part].t()).t())
+        check_product("dw", g["dw"][:, part], want, s, "bf16")
+    del x, y, saved, g
+    torch.cuda.empty_cache()
