@@ -331,7 +331,7 @@ struct MuonArgs {
   struct Phase {
     int a, b, out, add;
     float f, fd, fb;
-  } ph[2];
+  } ph;
 };
 static_assert(sizeof(MuonArgs) <= 4096, "kernel arguments");
 __host__ __device__ inline int64_t muon_pad(int64_t v) { return (v + kMuonPad - 1) / kMuonPad * kMuonPad; }
@@ -363,8 +363,8 @@ struct MuonSmall {
 hipError_t launch_muon_small(const MuonArgs& a, const MuonSmall& c, int p_dtype, int g_dtype, bool master, hipStream_t st);
 hipError_t launch_muon_momentum(const MuonArgs& a, uint32_t blocks, int g_dtype, hipStream_t st);
 hipError_t launch_muon_scale(const MuonArgs& a, uint32_t blocks, int g_dtype, hipStream_t st);
-// tile: 64, 128 or 256; phases: 1 or 2 products in one launch
-hipError_t launch_muon_square(const MuonArgs& a, uint32_t blocks, int tile, int phases, bool split, hipStream_t st);
+// tile: 64, 128 or 256
+hipError_t launch_muon_square(const MuonArgs& a, uint32_t blocks, int tile, bool split, hipStream_t st);
 hipError_t launch_muon_join(const MuonArgs& a, uint32_t blocks, hipStream_t st);
 hipError_t launch_muon_apply(const MuonArgs& a, uint32_t blocks, int tile, bool last, int p_dtype, bool master,
                              hipStream_t st);

@@ -17,7 +17,7 @@
 // alone (or bf16) leaves 2.7e-2 rms of an update of low rank, pairs 2e-5, as fp32
 // does, at four times its rate.  fp16's range is kept by powers of two: X and G are
 // held times 2^14 (entries under 1.5, as singular values stay under 1.21), Q times
-// 2^13 (a = 3.4445), P times 2^10 (a^3 = 41).
+// 2^13 (a = 3.4445), Q2 Q1 times 2^10 (a^2 = 12).
 #include <type_traits>
 
 #include "deft_device.h"
@@ -535,7 +535,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BT == 256 ?
   extern __shared__ __align__(16) unsigned char smem[];
   const int k = item_of(a, blockIdx.x);
   const MuonItem& t = a.it[k];
-  const MuonArgs::Phase& ph = a.ph[blockIdx.y];
+  const MuonArgs::Phase& ph = a.ph;
   const uint32_t tiles = (uint32_t)((muon_pad(t.m) + BT - 1) / BT);
   uint32_t at = blockIdx.x - a.first[k], split = 0, ti, tj;
   if (SPLIT) {
@@ -614,7 +614,7 @@ __global__ __launch_bounds__(128) void k_muon_join(const MuonArgs a) {
   const MuonItem& t = a.it[k];
   uint32_t ti, tj;
   triangle(blockIdx.x - a.first[k], ti, tj);
-  const Operand out = operand_of(t, a.ph[0].out);
+  const Operand out = operand_of(t, a.ph.out);
   const int r = tid / 4, c = tid % 4 * 8;
   const int64_t row = (int64_t)ti * 32 + r, col = (int64_t)tj * 32 + c;
   const float* p = (const float*)(t.base + muon_parts(t.m, t.n)) + row * out.rows + col;
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(128) void k_muon_join(const MuonArgs a) {
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    v[e] *= a.ph[0].f;
+    v[e] *= a.ph.f;
     turned[c + e][r] = v[e];
   }
   out.put(row, col, v);
@@ -675,7 +675,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BT == 256 ?
   extern __shared__ __align__(16) unsigned char smem[];
   const int k = item_of(a, blockIdx.x);
   const MuonItem& t = a.it[k];
-  const MuonArgs::Phase& ph = a.ph[0];
+  const MuonArgs::Phase& ph = a.ph;
   if (LAST && skipped(a.control)) return;
   // tiles of a column of X follow each other: they share it in the L2
   const uint32_t tiles_m = (uint32_t)((muon_pad(t.m) + BT - 1) / BT), at = blockIdx.x - a.first[k];
@@ -1000,9 +1000,9 @@ hipError_t big_lds(K kernel, int lds) {
 }
 
 template <int BT>
-hipError_t square(const MuonArgs& a, uint32_t blocks, int phases, bool split, hipStream_t st) {
+hipError_t square(const MuonArgs& a, uint32_t blocks, bool split, hipStream_t st) {
   constexpr int lds = Tile<BT>::kLds;
-  const dim3 grid(blocks, phases);
+  const dim3 grid(blocks);
   hipError_t e = split ? big_lds(k_muon_square<BT, true>, lds) : big_lds(k_muon_square<BT, false>, lds);
   if (e != hipSuccess) return e;
   if (split) DEFT_LAUNCH("muon_gram", (k_muon_square<BT, true>), grid, dim3(256), lds, st, a);
@@ -1054,10 +1054,10 @@ hipError_t launch_muon_scale(const MuonArgs& a, uint32_t blocks, int g_dtype, hi
   return hipGetLastError();
 }
 
-hipError_t launch_muon_square(const MuonArgs& a, uint32_t blocks, int tile, int phases, bool split, hipStream_t st) {
-  if (tile == 64) return square<64>(a, blocks, phases, split, st);
-  if (tile == 128) return square<128>(a, blocks, phases, split, st);
-  return square<256>(a, blocks, phases, split, st);
+hipError_t launch_muon_square(const MuonArgs& a, uint32_t blocks, int tile, bool split, hipStream_t st) {
+  if (tile == 64) return square<64>(a, blocks, split, st);
+  if (tile == 128) return square<128>(a, blocks, split, st);
+  return square<256>(a, blocks, split, st);
 }
 
 hipError_t launch_muon_join(const MuonArgs& a, uint32_t blocks, hipStream_t st) {

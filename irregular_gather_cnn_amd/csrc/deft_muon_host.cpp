@@ -145,48 +145,48 @@ struct Launcher {
 
   void gram(int x, int out) {
     if (e != hipSuccess) return;
-    a.ph[0] = {x, x, out, -1, (float)(kSg / (kSx * kSx)), 0.f, 0.f};
+    a.ph = {x, x, out, -1, (float)(kSg / (kSx * kSx)), 0.f, 0.f};
     const uint32_t n = lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, c.gram) * (c.split ? i.splits : 1); });
-    e = deft::launch_muon_square(a, n, c.gram, 1, c.split, st);
+    e = deft::launch_muon_square(a, n, c.gram, c.split, st);
     if (e != hipSuccess || !c.split) return;
     e = deft::launch_muon_join(a, lay(a, [](const deft::MuonItem& i) { return square_tiles(i.m, 32); }), st);
   }
-  void squares(int phases) {
+  void squares() {
     if (e != hipSuccess) return;
     e = deft::launch_muon_square(a, lay(a, [&](const deft::MuonItem& i) { return square_tiles(i.m, c.square); }), c.square,
-                                 phases, false, st);
+                                 false, st);
   }
   void apply(int p, double scale, int x, int out, bool last) {
     if (e != hipSuccess) return;
-    a.ph[0] = {p, x, out, -1, (float)(last ? 1.0 / (scale * kSx) : 1.0 / scale), 0.f, 0.f};
+    a.ph = {p, x, out, -1, (float)(last ? 1.0 / (scale * kSx) : 1.0 / scale), 0.f, 0.f};
     e = deft::launch_muon_apply(a, lay(a, [&](const deft::MuonItem& i) { return apply_tiles(i.m, i.n, c.apply); }), c.apply,
                                 last, p_dtype, master, st);
   }
 
-  // `steps` <= 3 of them on the X in buffer x; the result goes to the other one, or to the weights.
+  // One or two steps on the X in buffer x; the result goes to the other one, or to the
+  // weights.
   void fused(int steps, int x, bool last) {
-    int g = 2, other = 5, p = -1;
-    double scale = kSq;
-    const int r = 6;
+    // buffers of the squares: G, Q1 and Q2, the second G, Q1 G, Q2 Q1
+    const int g = 2, q1 = 3, q2 = 4, g2 = 5, r = 6, both = 7;
+    auto poly = [&](int of, int to) {
+      a.ph = {of, of, to, of, (float)(kC * kSq / (kSg * kSg)), (float)(kA * kSq), (float)(kB * kSq / kSg)};
+      squares();
+    };
+    auto times = [&](int left, int right, int to, double factor) {
+      a.ph = {left, right, to, -1, (float)factor, 0.f, 0.f};
+      squares();
+    };
     gram(x, g);
-    for (int k = 0; k < steps; ++k) {
-      // buffers of the squares: G 2 and 5 in turn, R 6, Q and P 3, 4, 7
-      const int q = k == 1 ? 4 : 3, to = k == 1 ? 7 : 4;
-      a.ph[0] = {g, g, q, g, (float)(kC * kSq / (kSg * kSg)), (float)(kA * kSq), (float)(kB * kSq / kSg)};
-      squares(1);
-      int n = 0;
-      if (k > 0) {
-        a.ph[n++] = {q, p, to, -1, (float)(k == 1 ? kSp / (kSq * kSq) : 1.0 / kSq), 0.f, 0.f};
-        scale = kSp;
-      }
-      p = k > 0 ? to : q;
-      if (k + 1 < steps) a.ph[n++] = {q, g, r, -1, (float)(1.0 / kSq), 0.f, 0.f};
-      if (n) squares(n);
-      if (k + 1 < steps) {
-        a.ph[0] = {q, r, other, -1, (float)(1.0 / kSq), 0.f, 0.f};
-        squares(1);
-        std::swap(g, other);
-      }
+    poly(g, q1);
+    int p = q1;
+    double scale = kSq;
+    if (steps == 2) {
+      times(q1, g, r, 1.0 / kSq);
+      times(q1, r, g2, 1.0 / kSq);
+      poly(g2, q2);
+      times(q2, q1, both, kSp / (kSq * kSq));
+      p = both;
+      scale = kSp;
     }
     apply(p, scale, x, 1 - x, last);
   }

@@ -439,17 +439,22 @@ template <typename T, int BM, int BN>
 hipError_t gemm(const Pw8GemmArgs& g, hipStream_t st) {
   const uint32_t blocks = (uint32_t)g.tiles_m * g.tiles_n * g.splits;
   constexpr int lds = Pw8Tile<BM, BN>::kLds;
-  hipError_t e = hipFuncSetAttribute(g.part ? (const void*)k_pw8_gemm<T, BM, BN, true> : (const void*)k_pw8_gemm<T, BM, BN, false>,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  // large tiles are taken where they fill the units, and not split
+  constexpr bool kSplits = BM * BN < 256 * 256;
+  const void* kernel = (const void*)k_pw8_gemm<T, BM, BN, false>;
+  if constexpr (kSplits) kernel = g.part ? (const void*)k_pw8_gemm<T, BM, BN, true> : kernel;
+  hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  if (g.part) {
+  if (!g.part) {
+    DEFT_LAUNCH("pw8_gemm", (k_pw8_gemm<T, BM, BN, false>), dim3(blocks), dim3(256), lds, st, g);
+    return hipGetLastError();
+  }
+  if constexpr (kSplits) {
     DEFT_LAUNCH("pw8_gemm", (k_pw8_gemm<T, BM, BN, true>), dim3(blocks), dim3(256), lds, st, g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t runs = g.out.rows * (g.part_cols / 8);
     DEFT_LAUNCH("pw8_join", k_pw8_join<T>, dim3((uint32_t)((runs + 255) / 256)), dim3(256), 0, st, g.out, g.part, g.splits,
                 g.part_cols);
-  } else {
-    DEFT_LAUNCH("pw8_gemm", (k_pw8_gemm<T, BM, BN, false>), dim3(blocks), dim3(256), lds, st, g);
   }
   return hipGetLastError();
 }

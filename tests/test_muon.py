@@ -217,7 +217,7 @@ def test_small_matrices_among_large_ones(shape):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("shapes", [[(1024, 1100), (600, 2300), (1500, 700)], [(2100, 2049)], [(300, 5000)] * 9,
-                                    [(40, 60000), (60000, 33)]])
+                                    [(40, 60000), (60000, 33)], [(6000, 6100)], [(1100, 9000), (9000, 1100)]])
 def test_large_tiles(shapes):
     check_direction([rand(s, 6 + k) for k, s in enumerate(shapes)])
     torch.cuda.empty_cache()

@@ -306,9 +306,10 @@ def test_few_rows_match_the_oracle(n, c_in, s, c_out, layout, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("n,c_in,s,c_out", [(8, 1024, 512, 4200), (1, 2048, 4097, 4225), (1, 520, 8300, 2050)])
-def test_large_tiles_match_the_oracle(n, c_in, s, c_out, dtype):
-    run_and_check(n, c_in, s, c_out, "channels_last", dtype)
+def test_large_tiles_match_the_oracle(n, c_in, s, c_out, layout, dtype):
+    run_and_check(n, c_in, s, c_out, layout, dtype)
     torch.cuda.empty_cache()
 
 
