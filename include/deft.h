@@ -460,7 +460,7 @@ size_t deft_grad_norm_workspace_bytes(int count);
  * (G from the smaller side).  m and p take one fp32 rounding per operation in this
  * order, p is rounded once to its dtype.  X is computed with 22 bits for each
  * factor and sums in fp32, as near to the formula's value as steps in fp32 are:
- * 2e-6 of its root mean square for matrices of normal values, 3e-5 where most
+ * 2e-6 of its root mean square for matrices of normal values, up to 5e-5 where most
  * singular values are small (their part of an error grows by up to 3.4 a step).
  * A zero direction leaves X zero; a NaN or an infinity in u makes all of p's
  * matrix NaN, and no other's.  Calls repeat their bits. */

@@ -346,7 +346,7 @@ inline int64_t muon_item_bytes(int m, int n, int splits) {
   return (muon_parts(m, n) + (splits > 1 ? splits * muon_square_bytes(m) : 0) + 255) / 256 * 256;
 }
 // Elements whose squares a workgroup sums, at most kMuonSums workgroups a matrix.
-inline int64_t muon_chunk(int64_t n) {
+__host__ __device__ inline int64_t muon_chunk(int64_t n) {
   const int64_t least = 4096, c = (n + kMuonSums - 1) / kMuonSums;
   return c <= least ? least : (c + 1023) / 1024 * 1024;
 }

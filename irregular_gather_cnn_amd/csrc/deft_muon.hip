@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void k_muon_momentum(const MuonArgs a) {
   const MuonItem& t = a.it[k];
   const int64_t all = (int64_t)t.m * t.n;
   const uint32_t share = blockIdx.x - a.first[k];
-  const int64_t least = (all + kMuonSums - 1) / kMuonSums, chunk = least <= 4096 ? 4096 : (least + 1023) / 1024 * 1024;
+  const int64_t chunk = muon_chunk(all);
   const int64_t i0 = share * chunk, i1 = min(all, i0 + chunk);
   const bool skip = skipped(a.control);
   const float coef = grad_factor(a.control);
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256) void k_muon_scale(const MuonArgs a) {
   const int tid = threadIdx.x;
   const int64_t mp = muon_pad(t.m), np = muon_pad(t.n);
   const int64_t all = (int64_t)t.m * t.n;
-  const int64_t least = (all + kMuonSums - 1) / kMuonSums, chunk = least <= 4096 ? 4096 : (least + 1023) / 1024 * 1024;
+  const int64_t chunk = muon_chunk(all);
   const int sums = (int)((all + chunk - 1) / chunk);
   double sum = tid < sums ? ((const double*)(t.base + muon_sums(t.m, t.n)))[tid] : 0.0;
 #pragma unroll
