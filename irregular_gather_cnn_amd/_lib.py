@@ -49,7 +49,19 @@ class DeftError(RuntimeError):
         super().__init__(msg)
 
 
-class deft_desc(ctypes.Structure):
+class _Descriptor(ctypes.Structure):
+    """A descriptor that refuses numbers over its 32-bit fields: ctypes would keep their low bits, and the
+    library would take 2^32 + 5 positions for 5."""
+
+    def __init__(self, *values, **named):
+        fields = dict(zip((name for name, _ in self._fields_), values), **named)
+        for name, kind in self._fields_:
+            if kind is ctypes.c_int and not -(1 << 31) <= fields.get(name, 0) < 1 << 31:
+                raise ValueError("%s must fit 32 bits, got %r" % (name, fields[name]))
+        super().__init__(*values, **named)
+
+
+class deft_desc(_Descriptor):
     _fields_ = [(n, ctypes.c_int) for n in (
         "n", "c_in", "h", "w", "c_out", "kh", "kw", "stride_h", "stride_w", "pad_h", "pad_w", "dil_h",
         "dil_w", "offset_groups", "dtype")]
@@ -66,7 +78,7 @@ class deft_plan_info(ctypes.Structure):
                 ("gather_gemm", ctypes.c_int), ("bwd_halo", ctypes.c_int)]
 
 
-class deft_adamw_desc(ctypes.Structure):
+class deft_adamw_desc(_Descriptor):
     _fields_ = [("p_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int), ("state_bits", ctypes.c_int),
                 ("master", ctypes.c_int), ("step", ctypes.c_int64), ("lr", ctypes.c_double),
                 ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
@@ -78,12 +90,12 @@ class deft_adamw_tensor(ctypes.Structure):
         ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double)]
 
 
-class deft_norm_desc(ctypes.Structure):
+class deft_norm_desc(_Descriptor):
     _fields_ = [(k, ctypes.c_int) for k in ("n", "c", "s", "groups", "layout", "act", "dtype")] + [
         ("eps", ctypes.c_double)]
 
 
-class deft_muon_desc(ctypes.Structure):
+class deft_muon_desc(_Descriptor):
     _fields_ = [(k, ctypes.c_int) for k in ("p_dtype", "g_dtype", "master", "nesterov", "steps")] + [
         (k, ctypes.c_double) for k in ("lr", "momentum", "eps")]
 
@@ -94,7 +106,7 @@ class deft_muon_tensor(ctypes.Structure):
         ("scale", ctypes.c_double)]
 
 
-class deft_pw8_desc(ctypes.Structure):
+class deft_pw8_desc(_Descriptor):
     _fields_ = [(k, ctypes.c_int) for k in ("n", "s", "c_in", "c_out", "layout", "dtype", "training")]
 
 
