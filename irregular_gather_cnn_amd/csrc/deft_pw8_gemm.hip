@@ -387,7 +387,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
         } else {
           float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += g.out.positions ? bias[i * kPasses + u] : bias[e];
+          for (int e = 0; e < 8; ++e) {
+            // values, not the places of one array, to choose from: those would be compared number by number
+            const float of_row = bias[i * kPasses + u], of_column = bias[e];
+            v[e] += g.out.positions ? of_row : of_column;
+          }
           runs.put(row, v);
         }
       }
