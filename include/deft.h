@@ -517,9 +517,10 @@ int deft_muon_step(const deft_muon_desc* d, const deft_muon_tensor* t, int count
  * power is 2^e with the least whole e >= -127 for which most <= 448 * 2^e, and
  * each value is rounded to the nearest multiple, ties to even.  A NaN or an
  * infinity makes NaN of the sums that it enters, and of no others.  Products are
- * exact, sums fp32, results rounded once; calls repeat their bits.  bf16: within
- * each 8 consecutive terms, what lies under 2^-13 of the largest is cut off before
- * they are added (the 8-bit matrix instructions' sum), 1.5e-5 of a result. */
+ * exact, sums fp32 (sums under 2^-126 may be lost), results rounded once; calls
+ * repeat their bits.  bf16: within each 8 consecutive terms, what lies under 2^-13 of
+ * the largest is cut off before they are added (the 8-bit matrix instructions' sum),
+ * 1.5e-5 of a result. */
 #define DEFT_PW8_BLOCK 128
 
 typedef struct deft_pw8_desc {

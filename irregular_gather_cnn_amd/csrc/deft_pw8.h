@@ -1,10 +1,10 @@
 // Codes of the 8-bit pointwise convolution, shared by the kernels that make them.
 //
 // Block of values v: with most = max |v| over its finite ones, e is the least
-// whole number >= -127 for which most <= 448 * 2^e; code = v * 2^-e rounded to
-// the nearest e4m3, ties to even; the block's scale byte is e + 127.  A NaN or an
-// infinity becomes the code NaN, and so reaches the outputs that it enters and
-// no other.
+// whole number >= -127 for which most <= 448 * 2^e, or 0 where most = 0; code =
+// v * 2^-e rounded to the nearest e4m3, ties to even; the block's scale byte is
+// e + 127.  A NaN or an infinity becomes the code NaN, and so reaches the outputs
+// that it enters and no other.
 //
 // A matrix of codes over rows and a depth is stored by half blocks of the depth:
 // codes [ceil(depth / 128)][2][rows][64], the last block filled up with zeros, and
@@ -56,7 +56,7 @@ __device__ __forceinline__ float sum_across_16(float v) {
 // e + 127 of a block whose largest value has these bits.
 __device__ __forceinline__ int pw8_scale_byte(uint32_t most) {
   const int e = (int)(most >> 23) - 8 + ((most & 0x7fffffu) > 0x600000u);  // 448 = 1.75 * 2^8
-  return e < 0 ? 0 : e;
+  return most == 0 ? 127 : e < 0 ? 0 : e;
 }
 // 2^-e; the byte is at most 247.
 __device__ __forceinline__ float pw8_inverse_scale(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
@@ -71,9 +71,9 @@ __device__ __forceinline__ uint32_t pw8_codes4(float a, float b, float c, float 
 // a time with 13 bits below the largest of the 8, and cut the rest off; groups
 // are then added in fp32.  That leaves a result off by 1.5e-5 of itself (normal
 // values, 64 to 8192 terms), a hundredth of what its rounding to bf16 does, for
-// twice the rate of the 16-bit instructions.  fp32 results take those: codes are
-// bf16 values exactly, their powers of two included, and 16-bit instructions sum
-// exact products as fp32 does (3e-8).
+// twice the rate of the 16-bit instructions.  fp32 results take those: codes times
+// their powers of two are bf16 values, but at the ends of the range, and 16-bit
+// instructions sum exact products as fp32 does (3e-8).
 typedef int pw8_codes_t __attribute__((ext_vector_type(8)));
 
 // 8 codes of words 2u and 2u + 1 times 2^(byte - 127), as bf16.
@@ -87,6 +87,20 @@ __device__ __forceinline__ bf16x8_t pw8_wide(const pw8_codes_t& c, int u, int by
     const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * u + k], scale, true);
     v[4 * k] = lo[0]; v[4 * k + 1] = lo[1]; v[4 * k + 2] = hi[0]; v[4 * k + 3] = hi[1];
   }
+  return v;
+}
+
+// Whether every code times 2^(byte - 127) is a normal bf16 value: codes reach from
+// 2^-9 to 448.  Under the least such byte values would be lost, and over the
+// greatest a code of 256 be infinite.  Products with those blocks take the 8-bit
+// instructions, eight times, each with one code of every eight in place: nothing
+// is cut off, then.
+__device__ __forceinline__ bool pw8_fits_bf16(int byte) { return (uint32_t)(byte - 10) <= 236u; }
+__device__ __forceinline__ pw8_codes_t pw8_one_of_8(const pw8_codes_t& c, int which) {
+  const int mask = 0xff << 8 * (which & 3), even = which < 4 ? mask : 0, odd = mask ^ even;
+  pw8_codes_t v;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) v[w] = c[w] & (w & 1 ? odd : even);
   return v;
 }
 

@@ -133,9 +133,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_pw8_few(const Pw8FewArgs a) {
             if (!live) run[u].clear();
             const uint32_t m = max_across_16(run[u].most());
             byte = pw8_scale_byte(m);
-            // codes of zeros are zeros over any power
-            done = !__any(m >= 0x7f800000u || (m != 0 && byte == 0));
-            if (done) q = run[u].codes(byte > 0 ? byte : 1);
+            done = !__any(m >= 0x7f800000u || byte == 0);
+            if (done) q = run[u].codes(byte);
           }
         }
         if (!done) {
@@ -165,9 +164,15 @@ __global__ __launch_bounds__(64 * kWaves) void k_pw8_few(const Pw8FewArgs a) {
           if constexpr (sizeof(T) == 2) {
             acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, q, acc[f], 0, 0, 0, ws[u][f], 0, byte);
           } else {
+            if (__any(!pw8_fits_bf16(ws[u][f]) || !pw8_fits_bf16(byte))) {  // deft_pw8.h says why
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e)
+                acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pw8_one_of_8(w, e), q, acc[f], 0, 0, 0, ws[u][f], 0, byte);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pw8_wide(w, e, ws[u][f]), pw8_wide(q, e, byte), acc[f], 0, 0, 0);
+              for (int e = 0; e < 4; ++e)
+                acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pw8_wide(w, e, ws[u][f]), pw8_wide(q, e, byte), acc[f], 0, 0, 0);
+            }
           }
         }
       }

@@ -144,12 +144,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   const int stages = 2 * (kb1 - kb0);
 
   f32x16_t acc[MI][NI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   // 16 rows of 64 bytes a load; a piece's place in its row depends on the row
   const int lrow = lane >> 2;
@@ -163,10 +157,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   const uint32_t lds0 = lds_addr_of(smem);
 
   const uint64_t step_a = uniform64(g.a.rows * kHalf), step_b = uniform64(g.b.rows * kHalf);
-  uint64_t code_a = uniform64((uint64_t)(g.a.codes + (2 * kb0 * g.a.rows + m0) * kHalf));
-  uint64_t code_b = uniform64((uint64_t)(g.b.codes + (2 * kb0 * g.b.rows + n0) * kHalf));
+  const uint64_t code_a0 = uniform64((uint64_t)(g.a.codes + (2 * kb0 * g.a.rows + m0) * kHalf));
+  const uint64_t code_b0 = uniform64((uint64_t)(g.b.codes + (2 * kb0 * g.b.rows + n0) * kHalf));
   // the scales that this wave loads: even waves A's, odd ones B's
-  uint64_t scale = uniform64((uint64_t)(wave & 1 ? g.b.scales + kb0 * srows_b + n0 : g.a.scales + kb0 * srows_a + m0));
+  const uint64_t scale0 = uniform64((uint64_t)(wave & 1 ? g.b.scales + kb0 * srows_b + n0 : g.a.scales + kb0 * srows_a + m0));
+  uint64_t code_a, code_b, scale;
   const uint64_t step_s = uniform64(wave & 1 ? srows_b : srows_a);
   const uint32_t bytes_s = wave & 1 ? scales_b : scales_a;
 
@@ -238,6 +233,30 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   auto multiply = [&](const Frags& f, int i, int j, const int* xa, const int* xb) {
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[j], f.a[i], acc[i][j], 0, 0, 0, xb[j], 0, xa[i]);
   };
+  // fp32, powers that do not fit bf16: one code of every eight at a time (deft_pw8.h)
+  auto multiply_apart = [&](const Frags& f, const int* xa, const int* xb) {
+#pragma unroll 1
+    for (int which = 0; which < 8; ++which)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const pw8_codes_t b = pw8_one_of_8(f.b[j], which);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, f.a[i], acc[i][j], 0, 0, 0, xb[j], 0, xa[i]);
+      }
+  };
+  // fp32: whether there is a power that does not fit bf16; rows past the last one have none
+  bool apart = false, row_a[MI], row_b[NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) row_a[i] = wm * MI * 32 + i * 32 + frow < ra;
+#pragma unroll
+  for (int j = 0; j < NI; ++j) row_b[j] = wn * NI * 32 + j * 32 + frow < rb;
+  auto look = [&](const int* xa, const int* xb) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) apart |= row_a[i] && !pw8_fits_bf16(xa[i]);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) apart |= row_b[j] && !pw8_fits_bf16(xb[j]);
+  };
   auto multiply_wide = [&](const Frags& f, const int* xa, const int* xb) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -275,8 +294,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   }
 
   Frags f[2];
-  auto step = [&](int s, auto odd_, auto full_) {
-    constexpr bool ODD = decltype(odd_)::value, FULL = decltype(full_)::value;
+  auto step = [&](int s, auto odd_, auto full_, auto apart_) {
+    constexpr bool ODD = decltype(odd_)::value, FULL = decltype(full_)::value, APART = decltype(apart_)::value;
     const Frags& now = f[ODD];
     Frags& next = f[!ODD];
     const bool more = FULL || s + 1 < stages, ahead = FULL || (s + 3 < stages && stages > 4);
@@ -294,7 +313,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
 #pragma unroll
         for (int u = 0; u < kFrags; ++u) read(s + 1, u, next);
       }
-      multiply_wide(now, sa[0], sb[0]);
+      if (APART) {
+        multiply_apart(now, sa[0], sb[0]);
+      } else {
+        if (!ODD) look(sa[0], sb[0]);
+        multiply_wide(now, sa[0], sb[0]);
+      }
     } else {
 #pragma unroll
       for (int t = 0; t < kSlots; ++t) {
@@ -330,30 +354,52 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
   using Yes = std::integral_constant<bool, true>;
   using No = std::integral_constant<bool, false>;
 
-  // three stages ahead, or all four that a short depth has; a block is two
-  load_scales(0);
+  auto run = [&](auto apart_) __attribute__((always_inline)) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    if (s < 3 ? s < stages : stages == 4) {
-      if (s == 2) load_scales(s);
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int u = 0; u < kFrags; ++u) load(s, u);
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    code_a = code_a0;
+    code_b = code_b0;
+    scale = scale0;
+    // three stages ahead, or all four that a short depth has; a block is two
+    load_scales(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s < 3 ? s < stages : stages == 4) {
+        if (s == 2) load_scales(s);
+#pragma unroll
+        for (int u = 0; u < kFrags; ++u) load(s, u);
+      }
     }
-  }
-  if (stages > 2) wait_vm<2 * C::kLoads + 1>();
-  else wait_vm<C::kLoads>();
-  meet();
-  read_scales(0, sa[0], sb[0]);
+    if (stages > 2) wait_vm<2 * C::kLoads + 1>();
+    else wait_vm<C::kLoads>();
+    meet();
+    read_scales(0, sa[0], sb[0]);
 #pragma unroll
-  for (int u = 0; u < kFrags; ++u) read(0, u, f[0]);
-  int s = 0;
-  for (; s + 4 < stages; s += 2) {
-    step(s, No(), Yes());
-    step(s + 1, Yes(), Yes());
-  }
-  for (; s < stages; s += 2) {
-    step(s, No(), No());
-    step(s + 1, Yes(), No());
+    for (int u = 0; u < kFrags; ++u) read(0, u, f[0]);
+    int s = 0;
+    for (; s + 4 < stages; s += 2) {
+      step(s, No(), Yes(), apart_);
+      step(s + 1, Yes(), Yes(), apart_);
+    }
+    for (; s < stages; s += 2) {
+      step(s, No(), No(), apart_);
+      step(s + 1, Yes(), No(), apart_);
+    }
+  };
+  run(No());
+  if constexpr (sizeof(T) == 4) {
+    __shared__ __align__(16) int met[4];
+    if (lane == 0) met[wave] = 0;
+    if (apart) met[wave] = 1;
+    __syncthreads();
+    // Once more from the start, if a wave has met powers that do not fit: 8192^3 takes
+    // 930 us, where one such value in x is met 2130. A branch in each step instead would
+    // leave the accumulators no registers (2200 spilled in the tile of 256 x 256).
+    if (met[0] | met[1] | met[2] | met[3]) run(Yes());
   }
   __syncthreads();
 
