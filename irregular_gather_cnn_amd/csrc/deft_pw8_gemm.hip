@@ -303,6 +303,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM * BN > 1
       if (more) {
         if (FULL || s + 2 < stages) wait_vm<C::kLoads + !ODD>();
         else wait_vm<0>();
+        // this wave's reads of stage s - 1, which loads go over, have ended, too: where the products
+        // that wait for them stand is left to the compiler
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         meet();
         if (ODD) read_scales(s + 1, sa[1], sb[1]);
         if (ahead) {
