@@ -199,10 +199,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
       uint2 c;
       c.x = pw8_codes4(pw8_scaled(v[i].get(0), inv), pw8_scaled(v[i].get(1), inv), pw8_scaled(v[i].get(2), inv), pw8_scaled(v[i].get(3), inv));
       c.y = pw8_codes4(pw8_scaled(v[i].get(4), inv), pw8_scaled(v[i].get(5), inv), pw8_scaled(v[i].get(6), inv), pw8_scaled(v[i].get(7), inv));
-      if (l0 + i < a.lines) {
-        *(uint2*)(a.near_codes + pw8_code(near_at, q / 8, a.lines, l0 + i) + q % 8 * kRun) = c;
-        if (q == 0) a.near_scales[(int64_t)near_at * pw8_scale_rows(a.lines) + l0 + i] = (uint8_t)byte;
-      }
+      if (l0 + i < a.lines) *(uint2*)(a.near_codes + pw8_code(near_at, q / 8, a.lines, l0 + i) + q % 8 * kRun) = c;
+      // the scales' rows past the last one are read, too
+      if (q == 0 && l0 + i < pw8_scale_rows(a.lines))
+        a.near_scales[(int64_t)near_at * pw8_scale_rows(a.lines) + l0 + i] = (uint8_t)byte;
     }
   }
   keep();
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
       // 8 lines of column b; columns of one j take the 8-byte places of a row of
       // the turned tile in different orders, so 16 threads write to 16 banks' pairs
       *(uint2*)(turned + b * kTile + ((t ^ q) << 3)) = c;
-      if (t == 0 && near0 + b < a.near)
+      if (t == 0 && near0 + b < pw8_scale_rows(a.near))
         a.far_scales[(int64_t)lines_at * pw8_scale_rows(a.near) + near0 + b] = (uint8_t)bytes[j];
     }
     __syncthreads();
