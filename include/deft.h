@@ -493,7 +493,9 @@ size_t deft_muon_workspace_bytes(const deft_muon_tensor* t, int count);
  * is what deft_grad_norm wrote: where it says that the gradients are not finite, the
  * step writes nothing but its workspace.  schedule (device, may be NULL): one
  * double, the lr that replaces the descriptor's, read when the kernels run.
- * count = 0 and matrices of no elements are allowed.
+ * count = 0 and matrices of no elements are allowed.  What a step writes, p, m and
+ * master of every matrix and the workspace, must not overlap, nor any gradient (not
+ * checked here).
  * DEFT_ERR_DTYPE; DEFT_ERR_BAD_DESC (a negative size, a rate out of range, masters
  * for fp32 weights); DEFT_ERR_UNSUPPORTED (a smaller side over 2^15, a larger one
  * over 2^22, over 2^32 elements); DEFT_ERR_NULLPTR; DEFT_ERR_ALIGN (tensors and workspace 16 bytes,

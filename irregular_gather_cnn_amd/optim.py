@@ -42,6 +42,14 @@ def _hold(tensors):
     return [t.untyped_storage() for t in tensors if t is not None]
 
 
+def _apart(tensors):
+    """Refuses (name, tensor) pairs that share memory: what a step writes to one it would write to another."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), what) for what, t in tensors if t.numel())
+    for (_, end, one), (start, _, other) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError("%s and %s share memory" % (one, other))
+
+
 class _Gradients:
     """The gradient buffers of a program: their sizes and dtype for good, the
     buffers themselves until :meth:`bind` names others."""
@@ -254,7 +262,8 @@ class Muon:
     (fp32 copies of bfloat16 params are made and updated, params are their rounded
     copies) or a list of fp32 tensors.  ``weight_decay``: one number or one per
     tensor.  ``states``: None (zeros) or a list of float32 momenta, updated in
-    place, as :attr:`states` of an earlier run.
+    place, as :attr:`states` of an earlier run.  Tensors that share memory which a
+    step writes are refused.
 
     The addresses of all tensors are taken here and in :meth:`bind`, and that
     memory is held: a tensor that is given other memory later on (``p.data =
@@ -275,9 +284,6 @@ class Muon:
             if p.dim() < 2:
                 raise ValueError("a param must have two dimensions or more, got %d" % p.dim())
         self.sizes = [p.numel() for p in self.params]
-        starts = [p.data_ptr() for p in self.params if p.numel()]
-        if len(set(starts)) < len(starts):
-            raise ValueError("a param is listed twice")
         self.shapes = [(p.shape[0], math.prod(p.shape[1:])) for p in self.params]
         self.grads = _Gradients(grads)
         if self.grads.sizes != self.sizes or self.grads.device != self.device:
@@ -297,6 +303,8 @@ class Muon:
                     if held[k] is None or held[k].numel() != n or held[k].dtype != torch.float32:
                         raise ValueError("%s %d must have %d elements of torch.float32" % (what, k, n))
                     _dense(held[k], "%s %d" % (what, k), self.index)
+        _apart(("%s %d" % (what, k), t) for what, held in (("param", self.params), ("state", self.states),
+                                                           ("master", self.masters or [])) for k, t in enumerate(held))
         self.lr = lr
         self._desc = _lib.deft_muon_desc(p_dtype, self.grads.dtype, 1 if self.masters else 0, 1 if nesterov else 0, steps,
                                          lr, momentum, eps)
