@@ -344,6 +344,13 @@ def deft_muon_workspace_bytes(tensors, count: int) -> int:
     return int(load().deft_muon_workspace_bytes(tensors, int(count)))
 
 
+def deft_muon_step(desc: deft_muon_desc, tensors, count: int, control=None, schedule=None, workspace=None, ws_bytes=0,
+                   stream=None) -> None:
+    """tensors: an array of deft_muon_tensor."""
+    _check(load().deft_muon_step(ctypes.byref(desc), tensors, int(count), _ptr(control), _ptr(schedule), _ptr(workspace),
+                                 int(ws_bytes), _ptr(stream)), "deft_muon_step")
+
+
 def deft_error_string(code: int) -> str:
     return load().deft_error_string(int(code)).decode()
 

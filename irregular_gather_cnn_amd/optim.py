@@ -303,11 +303,16 @@ class Muon:
                     if held[k] is None or held[k].numel() != n or held[k].dtype != torch.float32:
                         raise ValueError("%s %d must have %d elements of torch.float32" % (what, k, n))
                     _dense(held[k], "%s %d" % (what, k), self.index)
+        for k, d in enumerate(decay):
+            if not 0 <= d < math.inf:
+                raise ValueError("weight decay %d must be finite and not negative, got %r" % (k, d))
         _apart(("%s %d" % (what, k), t) for what, held in (("param", self.params), ("state", self.states),
                                                            ("master", self.masters or [])) for k, t in enumerate(held))
         self.lr = lr
         self._desc = _lib.deft_muon_desc(p_dtype, self.grads.dtype, 1 if self.masters else 0, 1 if nesterov else 0, steps,
                                          lr, momentum, eps)
+        # a list of nothing: what is wrong with the rates is said here, not at the first step
+        _lib.deft_muon_step(self._desc, None, 0)
         self._list = (_lib.deft_muon_tensor * len(self.params))()
         for k, (item, p) in enumerate(zip(self._list, self.params)):
             rows, cols = self.shapes[k]

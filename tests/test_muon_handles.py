@@ -1,7 +1,11 @@
-"""What Muon's constructor refuses: tensors that share memory which a step writes.  Without a GPU."""
+"""What Muon's constructor refuses: tensors that share memory which a step writes, and rates that no step takes.
+Without a GPU."""
+import math
+
 import pytest
 import torch
 
+from irregular_gather_cnn_amd import _lib as L
 from irregular_gather_cnn_amd.optim import Muon
 
 
@@ -40,3 +44,21 @@ def test_shared_memory(what):
     with pytest.raises(ValueError, match="memory|twice"):
         Muon(p, g, **more)
 
+@pytest.mark.parametrize("kw", [dict(steps=0), dict(steps=33), dict(momentum=1.0), dict(momentum=-0.1), dict(momentum=math.nan),
+                                dict(lr=-1.0), dict(lr=math.inf), dict(eps=0.0), dict(eps=math.nan)])
+def test_rates(kw):
+    with pytest.raises(L.DeftError):
+        Muon(*tensors(), **kw)
+
+
+@pytest.mark.parametrize("decay", [-0.1, math.nan, math.inf, [0.1, -0.1]])
+def test_weight_decay(decay):
+    with pytest.raises(ValueError, match="decay"):
+        Muon(*tensors(), weight_decay=decay)
+
+
+def test_masters_are_for_bf16():
+    with pytest.raises(L.DeftError):
+        Muon(*tensors(torch.float32), masters=[torch.zeros(24), torch.zeros(24)])
+    with pytest.raises(ValueError):  # float32 copies of float32 params are the params
+        Muon(*tensors(torch.float32), masters=True)
