@@ -462,6 +462,10 @@ size_t deft_grad_norm_workspace_bytes(int count);
  * factor and sums in fp32, as near to the formula's value as steps in fp32 are:
  * 2e-6 of its root mean square for matrices of normal values, up to 5e-5 where most
  * singular values are small (their part of an error grows by up to 3.4 a step).
+ * X is held in multiples of 2^-38, which five steps make 5e-10 of an element: where
+ * |u| is under 1e-4 eps, and the update tiny, that is more than those parts of it.
+ * A matrix's last bits may depend on the others of the list, whose sizes choose
+ * tiles and splits for all.
  * A zero direction leaves X zero; a NaN or an infinity in u makes all of p's
  * matrix NaN, and no other's.  Calls repeat their bits. */
 typedef struct deft_muon_desc {
