@@ -555,16 +555,16 @@ size_t deft_pw8_workspace_bytes(const deft_pw8_desc* d);
 int deft_pw8_pack(const deft_pw8_desc* d, const void* w, void* packed, void* stream);
 
 /* y; bias may be NULL.  training: writes `saved`, what the backward needs of x.
- * n * s = 0 is a no-op.  y must not overlap x.  Errors of all calls, besides the
- * descriptor's: DEFT_ERR_NULLPTR, DEFT_ERR_ALIGN (pointers 16 bytes),
- * DEFT_ERR_WORKSPACE, DEFT_ERR_BAD_DESC (an overlap; a backward without
- * training); checks run before any launch. */
+ * n * s = 0 is a no-op.  Errors of all calls, besides the descriptor's:
+ * DEFT_ERR_NULLPTR, DEFT_ERR_ALIGN (pointers 16 bytes), DEFT_ERR_WORKSPACE,
+ * DEFT_ERR_BAD_DESC (something written, the workspace included, over anything else
+ * that the call takes; a backward without training); checks run before any launch. */
 int deft_pw8_forward(const deft_pw8_desc* d, const void* x, const void* packed, const void* bias, void* y, void* saved,
                      void* workspace, size_t ws_bytes, void* stream);
 
 /* Gradients at dy, with `saved` as the forward left it and the packed weights
  * that it used; any of dx, dw and db may be NULL and is not computed then.  n * s
- * = 0 writes zeros to dw and db.  dx must not overlap dy. */
+ * = 0 writes zeros to dw and db. */
 int deft_pw8_backward(const deft_pw8_desc* d, const void* saved, const void* packed, const void* dy, void* dx, void* dw,
                       void* db, void* workspace, size_t ws_bytes, void* stream);
 

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "deft.h"
 #include "deft_internal.h"
@@ -27,6 +28,21 @@ int elem_size(int dtype) { return dtype == DEFT_BF16 ? 2 : 4; }
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
   return p && q && p < q + nb && q < p + na;
+}
+
+struct Span {
+  const void* p;  // nullptr: none
+  size_t bytes;
+};
+// Whether something that is written lies over anything else.
+bool overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* a = written.begin(); a != written.end(); ++a) {
+    for (const Span* b = a + 1; b != written.end(); ++b)
+      if (overlap(a->p, a->bytes, b->p, b->bytes)) return true;
+    for (const Span& b : read)
+      if (overlap(a->p, a->bytes, b.p, b.bytes)) return true;
+  }
+  return false;
 }
 
 // A matrix of codes inside a buffer.
@@ -195,6 +211,7 @@ hipError_t quantise(const deft_pw8_desc& d, int c, const void* x, char* rows_bas
 }
 
 size_t image_bytes(const deft_pw8_desc& d, int c) { return (size_t)d.n * d.s * c * elem_size(d.dtype); }
+size_t saved_bytes(const deft_pw8_desc& d) { return d.training ? part_at(0, d.c_in, (int64_t)d.n * d.s).end : 0; }
 
 }  // namespace
 
@@ -205,8 +222,7 @@ int deft_pw8_desc_validate(const deft_pw8_desc* d) { return desc_status(d); }
 size_t deft_pw8_packed_bytes(const deft_pw8_desc* d) { return desc_status(d) == DEFT_OK ? packed_of(*d).end : 0; }
 
 size_t deft_pw8_saved_bytes(const deft_pw8_desc* d) {
-  if (desc_status(d) != DEFT_OK || !d->training) return 0;
-  return part_at(0, d->c_in, (int64_t)d->n * d->s).end;
+  return desc_status(d) == DEFT_OK ? saved_bytes(*d) : 0;
 }
 
 size_t deft_pw8_workspace_bytes(const deft_pw8_desc* d) {
@@ -250,9 +266,11 @@ int deft_pw8_forward(const deft_pw8_desc* d, const void* x, const void* packed, 
   if (rows == 0) return DEFT_OK;
   if (!x || !packed || !y || (d->training && !saved)) return DEFT_ERR_NULLPTR;
   if (!aligned16(x) || !aligned16(packed) || !aligned16(bias) || !aligned16(y) || !aligned16(saved)) return DEFT_ERR_ALIGN;
-  if (overlap(x, image_bytes(*d, d->c_in), y, image_bytes(*d, d->c_out))) return DEFT_ERR_BAD_DESC;
-  const hipStream_t st = (hipStream_t)stream;
   const Packed p = packed_of(*d);
+  const Span out{y, image_bytes(*d, d->c_out)}, kept{d->training ? saved : nullptr, saved_bytes(*d)}, in{x, image_bytes(*d, d->c_in)};
+  const Span codes{packed, p.end}, biases{bias, (size_t)d->c_out * elem_size(d->dtype)};
+  if (overlap({out, kept}, {in, codes, biases})) return DEFT_ERR_BAD_DESC;
+  const hipStream_t st = (hipStream_t)stream;
   const int64_t positions = d->layout == DEFT_CHANNELS_FIRST ? d->s : 0;
   const int cus = deft::compute_units();
   if (few_rows(*d)) {
@@ -270,6 +288,7 @@ int deft_pw8_forward(const deft_pw8_desc* d, const void* x, const void* packed, 
   const Space w = forward_space(*d, rows, cus);
   if (!workspace || ws_bytes < w.end) return DEFT_ERR_WORKSPACE;
   if (!aligned16(workspace)) return DEFT_ERR_ALIGN;
+  if (overlap({{workspace, w.end}}, {out, kept, in, codes, biases})) return DEFT_ERR_BAD_DESC;
   char* ws = (char*)workspace;
   const Part keep = part_at(0, d->c_in, rows);
   hipError_t err = quantise(*d, d->c_in, x, ws, &w.a, (char*)saved, d->training ? &keep : nullptr, nullptr, st);
@@ -296,11 +315,16 @@ int deft_pw8_backward(const deft_pw8_desc* d, const void* saved, const void* pac
   }
   if ((dw && !saved) || (dx && !packed) || ((dx || dw || db) && !dy)) return DEFT_ERR_NULLPTR;
   if (!aligned16(saved) || !aligned16(packed) || !aligned16(dy)) return DEFT_ERR_ALIGN;
-  if (overlap(dx, image_bytes(*d, d->c_in), dy, image_bytes(*d, d->c_out))) return DEFT_ERR_BAD_DESC;
+  const Span in{dy, image_bytes(*d, d->c_out)}, of_x{dx, image_bytes(*d, d->c_in)};
+  if (overlap({of_x}, {in})) return DEFT_ERR_BAD_DESC;
   const int cus = deft::compute_units();
   const Space w = backward_space(*d, rows, cus);
   if (!workspace || ws_bytes < w.end) return DEFT_ERR_WORKSPACE;
   if (!aligned16(workspace)) return DEFT_ERR_ALIGN;
+  const size_t es = elem_size(d->dtype);
+  if (overlap({of_x, {dw, d->c_out * es * d->c_in}, {db, d->c_out * es}, {workspace, w.end}},
+              {in, {saved, saved_bytes(*d)}, {packed, packed_of(*d).end}}))
+    return DEFT_ERR_BAD_DESC;
   if (!dx && !dw && !db) return DEFT_OK;
   char* ws = (char*)workspace;
   float* sums = db ? (float*)(ws + w.sums) : nullptr;
