@@ -32,22 +32,6 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kScaleX = 16384.f;
 
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-  return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
-}
-// The pause: a load may read a scalar register that a vector instruction wrote
-// only five states later, and the compiler does not see the loads in the assembly.
-__device__ __forceinline__ rsrc_t uniform_rsrc(uint64_t p, uint32_t bytes) {
-  rsrc_t r;
-  r.x = (int)uniform((uint32_t)p);
-  r.y = (int)uniform((uint32_t)(p >> 32));
-  r.z = (int)uniform(bytes);
-  r.w = 0x00020000;
-  asm volatile("s_nop 4" : "+s"(r));
-  return r;
-}
-
 // Number of the matrix that a workgroup works on.
 __device__ __forceinline__ int item_of(const MuonArgs& a, uint32_t block) {
   const int lane = threadIdx.x & 63;
@@ -272,7 +256,7 @@ __global__ __launch_bounds__(256) void k_muon_scale(const MuonArgs a) {
 // of memory, in whole lines, whether the depth runs along the columns (squares and
 // Gram matrices) or the rows (X in P X).
 //
-// One workgroup of 2 x 2 waves makes a BT x BT tile of A B.  Stages of one to four
+// One workgroup of 2 x 2 waves makes a BT x BT tile of A B.  Stages of one or four
 // panels go straight into LDS in a ring of four.  A is read by rows; B by rows (its
 // transpose's columns), or, DEEP, as it lies, its fragments turned by
 // ds_read_b64_tr_b16.  16-byte pieces are XOR-swizzled so that the 16 rows of a
@@ -311,7 +295,7 @@ __device__ __forceinline__ void multiply(unsigned char* smem, const Operand a, c
                                          int64_t k0, int stages_of_two, f32x16_t (&acc)[BT / 64][BT / 64]) {
   using C = Tile<BT>;
   constexpr int MI = C::MI, kSlots = 3 * MI * MI;
-  const int stages = C::kSteps == 4 ? (stages_of_two + 1) / 2 : C::kSteps == 2 ? stages_of_two : 2 * stages_of_two;
+  const int stages = C::kSteps == 4 ? (stages_of_two + 1) / 2 : 2 * stages_of_two;
   // one block a wave: its three products a stage have sums of their own, as each
   // would wait for the one before
   constexpr int kSums = MI == 1 ? 3 : 1;
@@ -452,10 +436,8 @@ __device__ __forceinline__ void multiply(unsigned char* smem, const Operand a, c
       if (decltype(full)::value || s + 1 < stages) step(s + 1, std::integral_constant<int, 1>(), full);
     } else {
       step(s, std::integral_constant<int, 1>(), full);
-      if constexpr (kSteps == 4) {
-        step(s, std::integral_constant<int, 2>(), full);
-        step(s, std::integral_constant<int, 3>(), full);
-      }
+      step(s, std::integral_constant<int, 2>(), full);
+      step(s, std::integral_constant<int, 3>(), full);
     }
   };
 #pragma unroll
@@ -652,22 +634,6 @@ __device__ __forceinline__ void load_run(const float* p, float* f) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) { f[j] = a[j]; f[4 + j] = b[j]; }
 }
-__device__ __forceinline__ void store_run(bf16_t* p, const float* f) {
-  typedef uint32_t word4 __attribute__((ext_vector_type(4), aligned(2)));
-  word4 w;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-  *(word4*)p = w;
-}
-__device__ __forceinline__ void store_run(float* p, const float* f) {
-  typedef float word4 __attribute__((ext_vector_type(4), aligned(4)));
-  word4 a, b;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) { a[j] = f[j]; b[j] = f[4 + j]; }
-  *(word4*)p = a;
-  *(word4*)(p + 4) = b;
-}
-
 // X <- P X, or, LAST, p <- p (1 - lr wd) - lr s (P X).
 template <int BT, bool LAST, typename T, bool MASTER>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BT == 256 ? 1 : 2))) void k_muon_apply(const MuonArgs a) {

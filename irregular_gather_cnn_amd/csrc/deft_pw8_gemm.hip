@@ -26,42 +26,6 @@ __device__ __forceinline__ void load_lds4(const rsrc_t r, uint32_t lds_addr, int
                : "memory");
 }
 
-// A number that all lanes have, computed in vector registers (quotients, 64-bit
-// minima), for the scalar resources.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-  return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
-}
-
-// The pause: a load may read a scalar register that a vector instruction wrote
-// only five states later, and the compiler does not see the loads in the assembly.
-__device__ __forceinline__ rsrc_t uniform_rsrc(uint64_t p, uint32_t bytes) {
-  rsrc_t r;
-  r.x = (int)uniform((uint32_t)p);
-  r.y = (int)uniform((uint32_t)(p >> 32));
-  r.z = (int)uniform(bytes);
-  r.w = 0x00020000;
-  asm volatile("s_nop 4" : "+s"(r));
-  return r;
-}
-
-// 8 consecutive outputs, at any element address.
-__device__ __forceinline__ void store_run(bf16_t* p, const float* f) {
-  typedef uint32_t word4 __attribute__((ext_vector_type(4), aligned(2)));
-  word4 w;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-  *(word4*)p = w;
-}
-__device__ __forceinline__ void store_run(float* p, const float* f) {
-  typedef float word4 __attribute__((ext_vector_type(4), aligned(4)));
-  word4 a, b;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) { a[j] = f[j]; b[j] = f[4 + j]; }
-  *(word4*)p = a;
-  *(word4*)(p + 4) = b;
-}
-
 // Where a lane's runs of 8 columns go: column j of row 0, and on from row to row.
 // positions: columns run over the positions of all images, rows over channels
 // (channels first); else row-major.  A run that passes the last column or an
