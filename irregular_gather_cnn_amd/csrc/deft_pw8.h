@@ -69,9 +69,10 @@ __device__ __forceinline__ uint32_t pw8_codes4(float a, float b, float c, float 
 
 // How the products are summed.  The 8-bit matrix instructions add 8 products at
 // a time with 13 bits below the largest of the 8, and cut the rest off; groups
-// are then added in fp32.  That leaves a result off by 1.5e-5 of itself (normal
-// values, 64 to 8192 terms), a hundredth of what its rounding to bf16 does, for
-// twice the rate of the 16-bit instructions.  fp32 results take those: codes times
+// are then added in fp32.  That leaves results off by 1.5e-5 of their root mean
+// square (normal values, 64 to 8192 terms; 4.6e-5 where channels differ in size and
+// some values are large), where rounding to bf16 leaves 1.66e-3, for twice the rate
+// of the 16-bit instructions.  fp32 results take those: codes times
 // their powers of two are bf16 values, but at the ends of the range, and 16-bit
 // instructions sum exact products as fp32 does (3e-8).
 typedef int pw8_codes_t __attribute__((ext_vector_type(8)));

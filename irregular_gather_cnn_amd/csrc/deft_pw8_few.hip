@@ -203,8 +203,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_pw8_few(const Pw8FewArgs a) {
 template <typename T>
 hipError_t few(const Pw8FewArgs& a, int cus, hipStream_t st) {
   // 32 outputs a workgroup where that still leaves one for each compute unit: with 16 x is
-  // turned into codes twice as often (8 rows, 8192 to 8192: 21 us where they take 14.5,
-  // when that still took five times as many operations)
+  // turned into codes twice as often (8 rows, 8192 to 8192: 20.3 us where they take 14.5,
+  // fp32 28 and 22.5)
   constexpr int kAhead = sizeof(T) == 2 ? 4 : 1;
   if (a.w.rows >= (int64_t)32 * cus)
     DEFT_LAUNCH("pw8_few", (k_pw8_few<T, 2, kAhead>), dim3((uint32_t)((a.w.rows + 31) / 32)), dim3(64 * kWaves), 0, st, a);

@@ -70,10 +70,13 @@ struct Runs {
 // scale bytes), in a ring of four filled by loads straight into LDS.  The
 // fragments of the next stage are read, and a later one's loads issued, one or two
 // between two matrix instructions, so one wave a SIMD keeps its matrix unit fed: 8192^3
-// in 411 us, 2.7 PFLOP/s, where the instructions alone reach 3.5 on random values
-// (before, with the reads left to the compiler, 826).
-// 16-byte pieces are XOR-swizzled: the
-// 16 rows of a read's phase lie in 16 places of a 256-byte bank window.
+// in 411 to 470 us from card to card, 2.3 to 2.7 PFLOP/s, where the instructions alone
+// reach 3.5 on random values (461 us on a card where it takes 501 with reads and loads
+// after the barrier and their order left to the compiler, as products for fp32 have
+// them: those take 890, 1.2 PFLOP/s of the 16-bit instructions' 1.56).  What bounds it
+// is power: the clock falls to 1.8 GHz, and matrix units are busy 63 % of its cycles.
+// 16-byte pieces are XOR-swizzled: the 16 rows of a read's phase lie in 16 places of a
+// 256-byte bank window.
 template <int BM, int BN>
 struct Pw8Tile {
   static constexpr int MI = BM / 64, NI = BN / 64;      // 32 x 32 blocks of a wave

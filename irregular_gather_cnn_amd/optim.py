@@ -250,12 +250,12 @@ ADJUST = {
 
 
 class Muon:
-    """Momentum steps whose updates have their singular values brought near 1 by
-    ``steps`` Newton-Schulz steps, over ``params`` (device tensors of two or more
-    dimensions, all float32 or all bfloat16, updated in place; a matrix is the
-    first dimension by all others, as a convolution's weight is) and their gradient
-    buffers ``grads`` (likewise; read at every step, :meth:`bind` names others).
-    Biases and other vectors are for :class:`AdamW`.
+    """Muon (K. Jordan and others, 2024): momentum steps whose updates have their
+    singular values brought near 1 by ``steps`` Newton-Schulz steps, over ``params``
+    (device tensors of two or more dimensions, all float32 or all bfloat16, updated
+    in place; a matrix is the first dimension by all others, as a convolution's
+    weight is) and their gradient buffers ``grads`` (likewise; read at every step,
+    :meth:`bind` names others).  Biases and other vectors are for :class:`AdamW`.
 
     ``adjust``: the update's factor besides lr: "none", "aspect" (sqrt(max(1,
     rows / cols))) or "rms" (0.2 sqrt(max(rows, cols))).  ``masters``: None, True
