@@ -60,7 +60,8 @@ def pair(rows, c_in, c_out, dtype, kind, gen):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("n,s,c_in,c_out", [(4, 4, 500, 90), (1, 9, 130, 40), (3, 41, 300, 70), (2, 500, 640, 200),
-                                            (8, 1100, 200, 1500)])
+                                            (8, 1100, 200, 1500), (1, 60, 2100, 90), (1, 300, 2100, 90), (1, 50, 140, 33),
+                                            (1, 4200, 1000, 4100)])
 def test_forward(n, s, c_in, c_out, layout, dtype, kind):
     print("pw8 range", n, s, c_in, c_out, layout, dtype, kind, flush=True)
     x, w = pair(n * s, c_in, c_out, dtype, kind, torch.Generator(device="cuda").manual_seed(1))
@@ -74,9 +75,9 @@ def test_forward(n, s, c_in, c_out, layout, dtype, kind):
 @pytest.mark.parametrize("kind", ["large", "small", "mixed"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("layout", LAYOUTS)
-def test_gradients(layout, dtype, kind):
+@pytest.mark.parametrize("n,s,c_in,c_out", [(3, 200, 70, 300), (2, 1030, 40, 30)])
+def test_gradients(n, s, c_in, c_out, layout, dtype, kind):
     """dx from extreme dy, dw from extreme dy and x, in blocks of rows."""
-    n, s, c_in, c_out = 3, 200, 70, 300
     print("pw8 range gradients", layout, dtype, kind, flush=True)
     gen = torch.Generator(device="cuda").manual_seed(2)
     dy, wt = pair(n * s, c_out, c_in, dtype, kind, gen)  # dx sums over c_out
