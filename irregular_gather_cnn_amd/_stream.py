@@ -20,3 +20,20 @@ def elsewhere(index: int) -> bool:
     """Whether GPU `index` is not the current device.  The C ABI launches on the current one: every
     device's default stream has the handle 0."""
     return index >= 0 and _device() != index
+
+
+class Lent:
+    """Memory that a handle made for itself on one stream, used by calls on others.  Once the handle is gone torch
+    gives such memory to the first stream's next allocations, but for streams that it was told of."""
+
+    def __init__(self, index: int, tensors):
+        self.index, self.tensors = index, list(tensors)
+        self.streams = {current_stream(index) if index >= 0 else 0}
+
+    def to(self, stream: int) -> int:
+        """The stream, told of if it is new."""
+        if stream not in self.streams:
+            for t in self.tensors:
+                t.record_stream(torch.cuda.current_stream(self.index))
+            self.streams.add(stream)
+        return stream

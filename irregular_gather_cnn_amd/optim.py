@@ -15,7 +15,7 @@ import struct
 import torch
 
 from . import _lib
-from ._stream import current_stream, elsewhere
+from ._stream import Lent, current_stream, elsewhere
 
 # the fields of a deft_adamw_tensor, packed in a fifth of the time that its ctypes constructor takes
 _ITEM = struct.Struct("@7Pqd")
@@ -288,7 +288,8 @@ class Muon:
         self.grads = _Gradients(grads)
         if self.grads.sizes != self.sizes or self.grads.device != self.device:
             raise ValueError("the gradients' sizes and device must be those of the params")
-        if masters is True:
+        copied = masters is True
+        if copied:
             masters = [p.float() for p in self.params]
         self.masters = list(masters) if masters else None
         self.states = list(states) if states is not None else [
@@ -327,6 +328,9 @@ class Muon:
         self._call, self._ref, self._ws = _lib.load().deft_muon_step, ctypes.byref(self._desc), self.ws.data_ptr()
         self._norm = GradNorm.__new__(GradNorm)
         self._norm._setup(self.grads)
+        made = [self.ws, self._norm.ws, self._norm.control]
+        made += (self.states if states is None else []) + (self.masters if copied else [])
+        self._lent = Lent(self.index, made)
 
     def bind(self, grads):
         """From now on the gradients are read from these tensors."""
@@ -336,6 +340,8 @@ class Muon:
 
     def grad_norm(self, max_norm=float("inf"), inv_scale=1.0):
         """``control`` of the gradients (see :class:`GradNorm`), for :meth:`step`."""
+        if self.index >= 0:
+            self._lent.to(current_stream(self.index))
         return self._norm(max_norm, inv_scale)
 
     def step(self, control=None, lr=None, schedule=None):
@@ -354,6 +360,6 @@ class Muon:
         self._desc.lr = self.lr
         code = self._call(self._ref, self._list, len(self.params), None if control is None else control.data_ptr(),
                           None if schedule is None else schedule.data_ptr(), self._ws, self.ws_bytes,
-                          current_stream(self.index))
+                          self._lent.to(current_stream(self.index)))
         if code:
             raise _lib.DeftError(code, "deft_muon_step")

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._stream import current_stream, elsewhere
+from ._stream import Lent, current_stream, elsewhere
 
 
 class Pointwise8:
@@ -47,7 +47,7 @@ class Pointwise8:
         self.n, self.c_in, self.s, self.c_out, self.layout = n, c_in, s, c_out, layout
         self.tdtype, self.training = _DTYPES[dtype], bool(training)
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
-        self.device = self.ws.device
+        self.device, self._lent = self.ws.device, Lent(self._index, [self.ws])
         # what each argument must be: elements and dtype
         x, y, t = n * s * c_in, n * s * c_out, self.tdtype
         self._kinds = dict(x=(x, t), dx=(x, t), y=(y, t), dy=(y, t), w=(c_in * c_out, t), dw=(c_in * c_out, t),
@@ -105,7 +105,7 @@ class Pointwise8:
                 return self.forward(x, weights, b, y, saved)
         code = self._forward(self._ref, x.data_ptr(), weights.data_ptr(), None if b is None else b.data_ptr(),
                              y.data_ptr(), None if saved is None else saved.data_ptr(), self._ws, self.ws_bytes,
-                             current_stream(self._index))
+                             self._lent.to(current_stream(self._index)))
         if code:
             raise _lib.DeftError(code, "deft_pw8_forward")
         return y, saved
@@ -130,7 +130,7 @@ class Pointwise8:
         code = self._backward(self._ref, saved.data_ptr(), weights.data_ptr(), dy.data_ptr(),
                               None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
                               None if db is None else db.data_ptr(), self._ws, self.ws_bytes,
-                              current_stream(self._index))
+                              self._lent.to(current_stream(self._index)))
         if code:
             raise _lib.DeftError(code, "deft_pw8_backward")
         return out
